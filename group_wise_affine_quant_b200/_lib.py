@@ -15,7 +15,7 @@ STATUS_NAMES = {0: "AQ_OK", 1: "AQ_ERR_INVALID_ARG", 2: "AQ_ERR_UNSUPPORTED",
                 3: "AQ_ERR_MISALIGNED", 4: "AQ_ERR_CUDA", 5: "AQ_ERR_WORKSPACE"}
 AQ_F16, AQ_BF16 = 0, 1
 AQ_MODE_AFFINE, AQ_MODE_FP4 = 0, 1
-AQ_OP_QMV, AQ_OP_QMM, AQ_OP_QCONV2D, AQ_OP_QQMM, AQ_OP_QMM_NT = 0, 1, 2, 3, 4
+AQ_OP_QMV, AQ_OP_QMM, AQ_OP_QCONV2D, AQ_OP_QQMM, AQ_OP_QMM_NT, AQ_OP_QQMM_INT8 = range(6)
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -65,6 +65,24 @@ SIGNATURES["aq_gather_qmm"] = (_I, [_P, _P, _P, _P, _I32P, _I32P, _P, _I64, _I64
 SIGNATURES["aq_gather_qmm_workspace_size"] = (_SZ, [_I64, _I64, _I64, _I64, _I, _I, _I])
 SIGNATURES["aq_testing_gather_groups"] = (_I, [_I32P, _I32P, _I64, _I64, _I64, _I64, _I64, _I32P,
                                                _I32P, _I64, ctypes.POINTER(_I)])
+
+SIGNATURES["aq_quantize_int8"] = (_I, [_P, _P, _P, _I64, _I64, _I, _P])
+SIGNATURES["aq_int8_mm"] = (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P])
+SIGNATURES["aq_qqmm_int8"] = (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _SZ, _P])
+SIGNATURES["aq_testing_set_int8_plan"] = (None, [_I, _I, _I])
+
+
+class MoeMatrix(ctypes.Structure):
+    """aq_moe_matrix (include/aq.h)."""
+    _fields_ = [("w_q", _P), ("scales", _P), ("biases", _P)]
+
+
+_MM = ctypes.POINTER(MoeMatrix)
+SIGNATURES["aq_moe"] = (_I, [_P, _P, _MM, _MM, _MM, _P, _P, _P] + [_I64] * 5 +
+                        [_I, _I, _I, _I, _I, _P, _SZ, _P])
+SIGNATURES["aq_moe_experts"] = (_I, [_P, _P, _P, _MM, _MM, _MM, _P] + [_I64] * 5 +
+                                [_I, _I, _I, _I, _P, _SZ, _P])
+SIGNATURES["aq_moe_workspace_size"] = (_SZ, [_I64] * 5)
 
 _lib = None
 

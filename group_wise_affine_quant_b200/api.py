@@ -4,15 +4,20 @@ device memory and the current CUDA stream; every step of the computation runs
 in libaq.so's kernels.
 
 Tensors: x / w / y are fp16 or bf16 CUDA tensors; w_q is uint8 [N, K*bits/8];
-affine scales / biases are T [N, K/group_size]; FP4 scales are uint8.
+affine scales / biases are T [N, K/group_size]; FP4 scales are uint8.  The
+W8A8 functions take int8 codes and fp32 scales; the mixture-of-experts ones
+take stacks [E, ...] of the same weights.
 """
+import contextlib
+
 import torch
 
 from . import _lib
 from ._lib import (AQ_BF16, AQ_F16, AQ_MODE_AFFINE, AQ_MODE_FP4, AQ_OP_QCONV2D, AQ_OP_QMM,
-                   AQ_OP_QMM_NT, AQ_OP_QMV, AQ_OP_QQMM, AqError, check, lib)
+                   AQ_OP_QMM_NT, AQ_OP_QMV, AQ_OP_QQMM, AQ_OP_QQMM_INT8, AqError, check, lib)
 
 __all__ = ["aq_quantize", "aq_quantize_fp4", "aq_quantize_dequantize_fp", "aq_qqmm", "aq_dequantize", "aq_qmv", "aq_qmv_batched", "aq_qmm", "aq_qmm_nt", "aq_gather_qmm", "aq_qconv2d_nhwc",
+           "aq_quantize_int8", "aq_int8_mm", "aq_qqmm_int8", "aq_moe", "aq_moe_experts",
            "aq_workspace_size", "aq_qmv_noalloc", "aq_last_error", "aq_set_weight_prefetch",
            "aq_get_weight_prefetch", "aq_set_input_prefetch", "aq_get_input_prefetch", "AqError", "AQ_MODE_AFFINE", "AQ_MODE_FP4", "Workspace"]
 
@@ -282,4 +287,163 @@ def aq_qconv2d_nhwc(x, w_q, scales, biases, Cout, kh, kw, stride=(1, 1), pad=(0,
                                 groups, bits, group_size, _dt(x), _ptr(ws),
                                 0 if ws is None else ws.numel(), _stream(x.device)),
           "aq_qconv2d_nhwc")
+    return out
+
+
+def _tensor(name, t, dtype, *shape):
+    """Refuse a tensor the C call cannot take as it is (it sees only the address)."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _same_device(x, *others):
+    for t in others:
+        if t is not None and t.device != x.device:
+            raise ValueError("all tensors must be on one device, got %s and %s" % (x.device, t.device))
+
+
+def _matrix_shape(name, t):
+    if t.dim() != 2:
+        raise ValueError("%s must have 2 dimensions, got %d" % (name, t.dim()))
+    return t.shape
+
+
+_no_guard = contextlib.nullcontext()
+
+
+def _on(device):
+    """Make `device` the current one for a launch."""
+    return _no_guard if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def aq_quantize_int8(x, out=None):
+    """x [R, K] fp16/bf16 -> (codes int8 [R, K], scales fp32 [R]): a symmetric
+    scale per row (a token, or a channel of a weight)."""
+    R, K = _matrix_shape("x", x)
+    dt = _dt(x)
+    if out is None:
+        out = (torch.empty((R, K), dtype=torch.int8, device=x.device),
+               torch.empty((R,), dtype=torch.float32, device=x.device))
+    _same_device(x, *out)
+    px = _tensor("x", x, x.dtype, R, K)
+    pq, ps = _tensor("codes", out[0], torch.int8, R, K), _tensor("scales", out[1], torch.float32, R)
+    with _on(x.device):
+        check(lib().aq_quantize_int8(px, pq, ps, R, K, dt, _stream(x.device)), "aq_quantize_int8")
+    return out
+
+
+def aq_int8_mm(x_q, x_scales, w_q, w_scales, dtype=torch.bfloat16, out=None):
+    """y [M, N] = dtype(x_q . w_q^T * x_scales[:, None] * w_scales[None, :]) for
+    int8 x_q [M, K], w_q [N, K] and fp32 scales per token and channel."""
+    M, K = _matrix_shape("x_q", x_q)
+    N = _matrix_shape("w_q", w_q)[0]
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=x_q.device)
+    dt = _dt(out)
+    _same_device(x_q, x_scales, w_q, w_scales, out)
+    px, pxs = _tensor("x_q", x_q, torch.int8, M, K), _tensor("x_scales", x_scales, torch.float32, M)
+    pw, pws = _tensor("w_q", w_q, torch.int8, N, K), _tensor("w_scales", w_scales, torch.float32, N)
+    py = _tensor("out", out, out.dtype, M, N)
+    with _on(x_q.device):
+        check(lib().aq_int8_mm(px, pxs, pw, pws, py, M, N, K, dt, _stream(x_q.device)), "aq_int8_mm")
+    return out
+
+
+def aq_qqmm_int8(x, w_q, w_scales, out=None, workspace=None):
+    """W8A8: y [M, N] = x . w^T with the rows of x [M, K] fp16/bf16 quantized on
+    the way and an int8 weight w_q [N, K] with fp32 scales per channel."""
+    M, K = _matrix_shape("x", x)
+    N = _matrix_shape("w_q", w_q)[0]
+    dt = _dt(x)
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    _same_device(x, w_q, w_scales, out)
+    px, py = _tensor("x", x, x.dtype, M, K), _tensor("out", out, x.dtype, M, N)
+    pw, pws = _tensor("w_q", w_q, torch.int8, N, K), _tensor("w_scales", w_scales, torch.float32, N)
+    L = lib()
+    with _on(x.device):
+        ws = (workspace or _default_ws).get(
+            x.device, L.aq_workspace_size(AQ_OP_QQMM_INT8, M, N, K, 8, 16, AQ_MODE_AFFINE, 1))
+        check(L.aq_qqmm_int8(px, pw, pws, py, M, N, K, dt, _ptr(ws), 0 if ws is None else ws.numel(),
+                             _stream(x.device)), "aq_qqmm_int8")
+    return out
+
+
+def _moe_matrix(name, m, E, N, K, bits, group_size, dtype, device):
+    """(w_q, scales, biases) of one stack, checked -> the C struct and its mode."""
+    w_q, scales, biases = m
+    _same_device(w_q, scales, biases)
+    if w_q.device != device:
+        raise ValueError("%s is on %s, x on %s" % (name, w_q.device, device))
+    mode = _mode(scales)
+    G = K // group_size if group_size > 0 else 0
+    pw = _tensor(name + " w_q", w_q, torch.uint8, E, N, K * bits // 8)
+    ps = _tensor(name + " scales", scales, torch.uint8 if mode == AQ_MODE_FP4 else dtype, E, N, G)
+    pb = None if biases is None else _tensor(name + " biases", biases, dtype, E, N, G)
+    return _lib.MoeMatrix(pw, ps, pb), mode
+
+
+def _moe_args(x, gate, up, down, bits, group_size, out):
+    T, H = _matrix_shape("x", x)
+    dt = _dt(x)
+    if gate[0].dim() != 3:
+        raise ValueError("gate w_q must have 3 dimensions, got %d" % gate[0].dim())
+    E, I = gate[0].shape[0], gate[0].shape[1]
+    px = _tensor("x", x, x.dtype, T, H)
+    f = (bits, group_size, x.dtype, x.device)
+    g, mode = _moe_matrix("gate", gate, E, I, H, *f)
+    u, mode_u = _moe_matrix("up", up, E, I, H, *f)
+    d, mode_d = _moe_matrix("down", down, E, H, I, *f)
+    if not mode == mode_u == mode_d:
+        raise ValueError("gate, up and down must have one format")
+    if out is None:
+        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+    _same_device(x, out)
+    py = _tensor("out", out, x.dtype, T, H)
+    return T, H, I, E, dt, mode, px, (g, u, d), out, py
+
+
+def aq_moe(x, w_router, gate, up, down, top_k, normalize=True, bits=4, group_size=64, out=None,
+           workspace=None):
+    """A mixture-of-experts layer for T <= 64 tokens: x [T, H], w_router [E, H],
+    gate / up (w_q [E, I, H*bits/8], scales and biases [E, I, H/group_size],
+    biases None for FP4), down likewise [E, H, I...].  Returns (y [T, H],
+    indices int32 [T, top_k], weights fp32 [T, top_k])."""
+    T, H, I, E, dt, mode, px, (g, u, d), out, py = _moe_args(x, gate, up, down, bits, group_size, out)
+    _same_device(x, w_router)
+    pr = _tensor("w_router", w_router, x.dtype, E, H)
+    k = max(int(top_k), 0)
+    indices = torch.empty((T, k), dtype=torch.int32, device=x.device)
+    weights = torch.empty((T, k), dtype=torch.float32, device=x.device)
+    L = lib()
+    with _on(x.device):
+        ws = (workspace or _default_ws).get(x.device, L.aq_moe_workspace_size(T, H, I, E, k))
+        check(L.aq_moe(px, pr, g, u, d, py, indices.data_ptr(), weights.data_ptr(), T, H, I, E,
+                       top_k, 1 if normalize else 0, bits, group_size, mode, dt, _ptr(ws),
+                       0 if ws is None else ws.numel(), _stream(x.device)), "aq_moe")
+    return out, indices, weights
+
+
+def aq_moe_experts(x, indices, weights, gate, up, down, bits=4, group_size=64, out=None,
+                   workspace=None):
+    """The experts of aq_moe for given routing: indices int32 [T, k] and weights
+    fp32 [T, k] on the device (an index outside 0..E-1 skips its slot)."""
+    T, H, I, E, dt, mode, px, (g, u, d), out, py = _moe_args(x, gate, up, down, bits, group_size, out)
+    k = _matrix_shape("indices", indices)[1]
+    _same_device(x, indices, weights)
+    pi = _tensor("indices", indices, torch.int32, T, k)
+    pw = _tensor("weights", weights, torch.float32, T, k)
+    L = lib()
+    with _on(x.device):
+        ws = (workspace or _default_ws).get(x.device, L.aq_moe_workspace_size(T, H, I, E, k))
+        check(L.aq_moe_experts(px, pi, pw, g, u, d, py, T, H, I, E, k, bits, group_size, mode, dt,
+                               _ptr(ws), 0 if ws is None else ws.numel(), _stream(x.device)),
+              "aq_moe_experts")
     return out

@@ -625,6 +625,214 @@ aq_status aq_qqmm(const void* x, const void* w_q, const void* scales, void* y, i
   return st;
 }
 
+// ------------------------------------------------------------------- W8A8
+// K limit of the integer product: with codes of any value (-128 * -128 =
+// 2^14) the sum stays inside 32 bits.
+static const int64_t kMaxInt8K = ((int64_t)1 << 17) - 1;
+static const int64_t kMaxInt8Dim = (int64_t)1 << 30;
+
+static aq_status check_int8_sizes(int64_t M, int64_t N, int64_t K, aq_dtype dtype) {
+  if (dtype != AQ_F16 && dtype != AQ_BF16)
+    return fail(AQ_ERR_UNSUPPORTED, "dtype %d is not fp16 (0) or bf16 (1)", (int)dtype);
+  if (M < 0 || N < 0 || M > kMaxInt8Dim || N > kMaxInt8Dim)
+    return fail(AQ_ERR_INVALID_ARG, "M=%lld N=%lld out of range", (long long)M, (long long)N);
+  if (K < 0 || K > kMaxInt8K)
+    return fail(AQ_ERR_INVALID_ARG, "K=%lld: 0 <= K <= %lld (a 32-bit sum of 8-bit products)",
+                (long long)K, (long long)kMaxInt8K);
+  if (K % 16) return fail(AQ_ERR_INVALID_ARG, "K=%lld is not a multiple of 16", (long long)K);
+  return AQ_OK;
+}
+
+aq_status aq_quantize_int8(const void* x, void* x_q, float* scales, int64_t rows, int64_t K,
+                           aq_dtype dtype, aq_stream_t stream) {
+  g_err[0] = 0;
+  if (dtype != AQ_F16 && dtype != AQ_BF16)
+    return fail(AQ_ERR_UNSUPPORTED, "dtype %d is not fp16 (0) or bf16 (1)", (int)dtype);
+  if (rows < 0 || rows > kMaxInt8Dim || K < 0 || K > kMaxDim)
+    return fail(AQ_ERR_INVALID_ARG, "rows=%lld K=%lld out of range", (long long)rows, (long long)K);
+  if (K % 16) return fail(AQ_ERR_INVALID_ARG, "K=%lld is not a multiple of 16", (long long)K);
+  if (rows == 0) return AQ_OK;
+  if (!scales) return fail(AQ_ERR_INVALID_ARG, "scales must not be NULL");
+  if (!aligned(scales, 4)) return fail(AQ_ERR_MISALIGNED, "scales must be 4-byte aligned");
+  if (K == 0)
+    return cuda_status(cudaMemsetAsync(scales, 0, (size_t)rows * 4, (cudaStream_t)stream),
+                       "zero-fill of scales");
+  if (!x || !x_q) return fail(AQ_ERR_INVALID_ARG, "x and x_q must not be NULL");
+  if (!aligned(x, 16) || !aligned(x_q, 16))
+    return fail(AQ_ERR_MISALIGNED, "x and x_q must be 16-byte aligned");
+  return cuda_status(aq::launch_quantize_int8(x, x_q, scales, rows, K, dtype, (cudaStream_t)stream),
+                     "aq_quantize_int8 launch");
+}
+
+// Checks of the weight side and y, shared by aq_int8_mm and aq_qqmm_int8.
+static aq_status check_int8_weight(const void* w_q, const float* w_scales, const void* y) {
+  if (!y || !w_scales) return fail(AQ_ERR_INVALID_ARG, "w_scales and y must not be NULL");
+  if (!w_q) return fail(AQ_ERR_INVALID_ARG, "w_q must not be NULL");
+  if (!aligned(w_q, 16) || !aligned(y, 16))
+    return fail(AQ_ERR_MISALIGNED, "w_q and y must be 16-byte aligned");
+  if (!aligned(w_scales, 4)) return fail(AQ_ERR_MISALIGNED, "w_scales must be 4-byte aligned");
+  return AQ_OK;
+}
+
+aq_status aq_int8_mm(const void* x_q, const float* x_scales, const void* w_q,
+                     const float* w_scales, void* y, int64_t M, int64_t N, int64_t K,
+                     aq_dtype dtype, aq_stream_t stream) {
+  g_err[0] = 0;
+  aq_status st = check_int8_sizes(M, N, K, dtype);
+  if (st != AQ_OK) return st;
+  if (M == 0 || N == 0) return AQ_OK;
+  if (K == 0) {
+    if (!y) return fail(AQ_ERR_INVALID_ARG, "y must not be NULL");
+    return zero_output(y, M, N, stream);
+  }
+  if ((st = check_int8_weight(w_q, w_scales, y)) != AQ_OK) return st;
+  if (!x_q || !x_scales) return fail(AQ_ERR_INVALID_ARG, "x_q and x_scales must not be NULL");
+  if (!aligned(x_q, 16)) return fail(AQ_ERR_MISALIGNED, "x_q must be 16-byte aligned");
+  if (!aligned(x_scales, 4)) return fail(AQ_ERR_MISALIGNED, "x_scales must be 4-byte aligned");
+  return cuda_status(aq::launch_int8_mm(x_q, x_scales, w_q, w_scales, y, M, N, K, dtype,
+                                        g_weight_prefetch, (cudaStream_t)stream),
+                     "aq_int8_mm launch");
+}
+
+// Workspace of aq_qqmm_int8: the shared counter area (untouched), then the
+// codes of x and its scales.
+static size_t qqmm_int8_scales_at(int64_t M, int64_t K) { return 65536 + align256((size_t)(M * K)); }
+
+aq_status aq_qqmm_int8(const void* x, const void* w_q, const float* w_scales, void* y, int64_t M,
+                       int64_t N, int64_t K, aq_dtype dtype, void* workspace,
+                       size_t workspace_bytes, aq_stream_t stream) {
+  g_err[0] = 0;
+  aq_status st = check_int8_sizes(M, N, K, dtype);
+  if (st != AQ_OK) return st;
+  if (M == 0 || N == 0) return AQ_OK;
+  if (K == 0) {
+    if (!y) return fail(AQ_ERR_INVALID_ARG, "y must not be NULL");
+    return zero_output(y, M, N, stream);
+  }
+  if ((st = check_int8_weight(w_q, w_scales, y)) != AQ_OK) return st;
+  if (!x) return fail(AQ_ERR_INVALID_ARG, "x must not be NULL");
+  if (!aligned(x, 16)) return fail(AQ_ERR_MISALIGNED, "x must be 16-byte aligned");
+  const size_t need = aq_workspace_size(AQ_OP_QQMM_INT8, M, N, K, 8, 16, AQ_MODE_AFFINE, 1);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != AQ_OK) return st;
+  uint8_t* x_q = static_cast<uint8_t*>(workspace) + 65536;
+  float* x_scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                             qqmm_int8_scales_at(M, K));
+  st = cuda_status(aq::launch_quantize_int8(x, x_q, x_scales, M, K, dtype, (cudaStream_t)stream),
+                   "aq_qqmm_int8 quantizer launch");
+  if (st != AQ_OK) return st;
+  // The product may start while the quantizer runs, and the quantizer starts
+  // only after everything before it has ended: no kernel that still runs then
+  // writes the weights, so they are read early whatever the thread's setting.
+  return cuda_status(aq::launch_int8_mm(x_q, x_scales, w_q, w_scales, y, M, N, K, dtype, 1,
+                                        (cudaStream_t)stream),
+                     "aq_qqmm_int8 product launch");
+}
+
+// ------------------------------------------------------- mixture of experts
+static const int64_t kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 512,
+                     kMoeMaxWidth = 65536;
+
+static aq_status check_moe_matrix(const char* name, const aq_moe_matrix* m, aq_mode mode) {
+  if (!m || !m->w_q || !m->scales)
+    return fail(AQ_ERR_INVALID_ARG, "%s: w_q and scales must not be NULL", name);
+  if (mode == AQ_MODE_AFFINE && !m->biases)
+    return fail(AQ_ERR_INVALID_ARG, "%s: affine mode needs biases", name);
+  if (mode == AQ_MODE_FP4 && m->biases)
+    return fail(AQ_ERR_INVALID_ARG, "%s: FP4 mode takes no biases (pass NULL)", name);
+  if (!aligned(m->w_q, 16) || !aligned(m->scales, 16) || !aligned(m->biases, 16))
+    return fail(AQ_ERR_MISALIGNED, "%s: w_q, scales and biases must be 16-byte aligned", name);
+  return AQ_OK;
+}
+
+static aq_status run_moe(const void* x, const void* w_router, int32_t* indices, float* weights,
+                         const aq_moe_matrix* gate, const aq_moe_matrix* up,
+                         const aq_moe_matrix* down, void* y, int64_t T, int64_t H, int64_t I,
+                         int64_t E, int64_t top_k, int normalize, int bits, int group_size,
+                         aq_mode mode, aq_dtype dtype, void* workspace, size_t workspace_bytes,
+                         aq_stream_t stream, const char* what) {
+  aq_status st = check_format(bits, group_size, mode, dtype);
+  if (st != AQ_OK) return st;
+  if (T < 0 || T > kMoeMaxTokens)
+    return fail(AQ_ERR_INVALID_ARG, "T=%lld: at most %lld tokens", (long long)T,
+                (long long)kMoeMaxTokens);
+  if (E < 1 || E > kMoeMaxExperts)
+    return fail(AQ_ERR_INVALID_ARG, "E=%lld: 1 to %lld experts", (long long)E,
+                (long long)kMoeMaxExperts);
+  if (top_k < 1 || top_k > kMoeMaxTopK || (w_router && top_k > E))
+    return fail(AQ_ERR_INVALID_ARG, "top_k=%lld: 1 to %lld, and at most E=%lld experts a token",
+                (long long)top_k, (long long)kMoeMaxTopK, (long long)E);
+  const int64_t unit = group_size > 32 ? group_size : 32;
+  if (H < 1 || I < 1 || H > kMoeMaxWidth || I > kMoeMaxWidth || H % unit || I % unit)
+    return fail(AQ_ERR_INVALID_ARG, "H=%lld I=%lld: positive multiples of %lld up to %lld",
+                (long long)H, (long long)I, (long long)unit, (long long)kMoeMaxWidth);
+  if (T == 0) return AQ_OK;
+  if ((st = check_moe_matrix("gate", gate, mode)) != AQ_OK) return st;
+  if ((st = check_moe_matrix("up", up, mode)) != AQ_OK) return st;
+  if ((st = check_moe_matrix("down", down, mode)) != AQ_OK) return st;
+  if (!x || !y || !indices || !weights)
+    return fail(AQ_ERR_INVALID_ARG, "x, y, indices and weights must not be NULL");
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(w_router, 16))
+    return fail(AQ_ERR_MISALIGNED, "x, y and w_router must be 16-byte aligned");
+  if (!aligned(indices, 4) || !aligned(weights, 4))
+    return fail(AQ_ERR_MISALIGNED, "indices and weights must be 4-byte aligned");
+  st = check_workspace(workspace, workspace_bytes, aq::moe_workspace(T, H, I, E, top_k));
+  if (st != AQ_OK) return st;
+  auto matrix = [](const aq_moe_matrix* m) {
+    return aq::MoeMatrix{static_cast<const uint8_t*>(m->w_q), static_cast<const uint8_t*>(m->scales),
+                         static_cast<const uint8_t*>(m->biases)};
+  };
+  aq::MoeArgs a{};
+  a.x = x;
+  a.w_router = w_router;
+  a.indices = indices;
+  a.weights = weights;
+  a.gate = matrix(gate);
+  a.up = matrix(up);
+  a.down = matrix(down);
+  a.y = y;
+  a.T = (int)T;
+  a.H = (int)H;
+  a.I = (int)I;
+  a.E = (int)E;
+  a.top_k = (int)top_k;
+  a.normalize = normalize ? 1 : 0;
+  a.gs = group_size;
+  a.workspace = static_cast<uint8_t*>(workspace);
+  return cuda_status(aq::launch_moe(a, bits, mode, dtype, (cudaStream_t)stream), what);
+}
+
+aq_status aq_moe(const void* x, const void* w_router, const aq_moe_matrix* gate,
+                 const aq_moe_matrix* up, const aq_moe_matrix* down, void* y, int32_t* indices,
+                 float* weights, int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k,
+                 int normalize, int bits, int group_size, aq_mode mode, aq_dtype dtype,
+                 void* workspace, size_t workspace_bytes, aq_stream_t stream) {
+  g_err[0] = 0;
+  if (T > 0 && !w_router) return fail(AQ_ERR_INVALID_ARG, "w_router must not be NULL");
+  return run_moe(x, w_router, indices, weights, gate, up, down, y, T, H, I, E, top_k, normalize,
+                 bits, group_size, mode, dtype, workspace, workspace_bytes, stream,
+                 "aq_moe launch");
+}
+
+aq_status aq_moe_experts(const void* x, const int32_t* indices, const float* weights,
+                         const aq_moe_matrix* gate, const aq_moe_matrix* up,
+                         const aq_moe_matrix* down, void* y, int64_t T, int64_t H, int64_t I,
+                         int64_t E, int64_t top_k, int bits, int group_size, aq_mode mode,
+                         aq_dtype dtype, void* workspace, size_t workspace_bytes,
+                         aq_stream_t stream) {
+  g_err[0] = 0;
+  // without a router the kernel only reads indices and weights
+  return run_moe(x, nullptr, const_cast<int32_t*>(indices), const_cast<float*>(weights), gate, up,
+                 down, y, T, H, I, E, top_k, 0, bits, group_size, mode, dtype, workspace,
+                 workspace_bytes, stream, "aq_moe_experts launch");
+}
+
+size_t aq_moe_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
+  if (T < 1 || T > kMoeMaxTokens || E < 1 || E > kMoeMaxExperts || top_k < 1 ||
+      top_k > kMoeMaxTopK || H < 1 || H > kMoeMaxWidth || I < 1 || I > kMoeMaxWidth)
+    return 0;
+  return aq::moe_workspace(T, H, I, E, top_k);
+}
+
 int aq_testing_gather_groups(const int32_t* lhs_indices, const int32_t* rhs_indices,
                              int64_t n_pairs, int64_t M, int64_t N, int64_t K, int64_t x_batch,
                              int32_t* xmap, int32_t* ymap, int64_t map_rows, int* rows_per_group) {
@@ -641,6 +849,9 @@ int aq_testing_gather_groups(const int32_t* lhs_indices, const int32_t* rhs_indi
 
 void aq_testing_set_wait_limit_ns(uint64_t ns) { aq::testing_set_mv_wait_ns(ns); }
 void aq_testing_set_start_delay_ns(uint64_t ns) { aq::testing_set_mv_delay_ns(ns); }
+void aq_testing_set_int8_plan(int tokens, int pair, int splits) {
+  aq::testing_set_int8_plan(tokens, pair, splits);
+}
 void aq_testing_set_qmv_kernel(int which) { g_qmv_kernel.store(which, std::memory_order_relaxed); }
 aq_status aq_testing_clear_device_errors(void) {
   g_err[0] = 0;
@@ -656,7 +867,10 @@ unsigned aq_device_errors(void) {
   unsigned t = 0, u = 0;
   if (aq::read_device_error_qmv_tc(&t) != cudaSuccess) return 0xFFFFFFFFu;
   if (aq::read_device_error_qmv_mma(&u) != cudaSuccess) return 0xFFFFFFFFu;
-  return v | w | t | u;
+  unsigned i = 0, m = 0;
+  if (aq::read_device_error_int8(&i) != cudaSuccess) return 0xFFFFFFFFu;
+  if (aq::read_device_error_moe(&m) != cudaSuccess) return 0xFFFFFFFFu;
+  return v | w | t | u | i | m;
 }
 
 aq_status aq_qconv2d_nhwc(const void* x, const void* w_q, const void* scales,
@@ -700,6 +914,10 @@ aq_status aq_qconv2d_nhwc(const void* x, const void* w_q, const void* scales,
 size_t aq_workspace_size(aq_op op, int64_t M, int64_t N, int64_t K, int bits, int group_size,
                          aq_mode mode, int groups) {
   (void)groups;
+  if (op == AQ_OP_QQMM_INT8) {
+    if (M <= 0 || N <= 0 || K <= 0 || M > kMaxInt8Dim || K > kMaxInt8K) return 0;
+    return qqmm_int8_scales_at(M, K) + align256((size_t)M * 4);
+  }
   if (M <= 0 || N <= 0 || K <= 0 || group_size <= 0 || K % group_size) return 0;
   if (op == AQ_OP_QMV) {
     if (M > 16) return 0;

@@ -106,4 +106,43 @@ int weight_prefetch_enabled();
 // aq_set_input_prefetch's setting of the calling thread (0 or 1).
 int input_prefetch_enabled();
 cudaError_t read_device_error_conv(unsigned* out);
+
+// W8A8 (int8.cu): row quantizer and integer product.
+struct Int8Plan {
+  int bn;          // tokens per tile (MMA N)
+  bool pair;       // two CTAs share a tile of 256 channels
+  int splits;      // K-slices, one cluster per tile
+  int kb_split;    // 128-element blocks of K per slice
+  int64_t groups;  // CTA pairs, clusters or CTAs launched
+};
+Int8Plan plan_int8_mm(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_quantize_int8(const void* x, void* xq, float* scales, int64_t rows, int64_t K,
+                                 int dtype, cudaStream_t st);
+cudaError_t launch_int8_mm(const void* x_q, const float* x_scales, const void* w_q,
+                           const float* w_scales, void* y, int64_t M, int64_t N, int64_t K,
+                           int dtype, int prefetch, cudaStream_t st);
+cudaError_t read_device_error_int8(unsigned* out);
+void testing_set_int8_plan(int bn, int pair, int splits);
+
+// Mixture-of-experts layer for a few tokens (moe.cu).
+struct MoeMatrix {
+  const uint8_t* w_q;
+  const uint8_t* scales;
+  const uint8_t* biases;
+};
+struct MoeArgs {
+  const void* x;             // [T, H]
+  const void* w_router;      // [E, H], nullptr: indices / weights are inputs
+  int32_t* indices;          // [T, top_k]
+  float* weights;            // [T, top_k]
+  MoeMatrix gate, up, down;  // [E, I, H], [E, I, H], [E, H, I]
+  void* y;                   // [T, H]
+  int T, H, I, E, top_k;
+  int normalize;
+  int gs;
+  uint8_t* workspace;
+};
+size_t moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
+cudaError_t launch_moe(const MoeArgs& a, int bits, int mode, int dtype, cudaStream_t st);
+cudaError_t read_device_error_moe(unsigned* out);
 }  // namespace aq

@@ -77,7 +77,8 @@ typedef enum {
 } aq_mode;
 
 typedef enum {
-  AQ_OP_QMV = 0, AQ_OP_QMM = 1, AQ_OP_QCONV2D = 2, AQ_OP_QQMM = 3, AQ_OP_QMM_NT = 4
+  AQ_OP_QMV = 0, AQ_OP_QMM = 1, AQ_OP_QCONV2D = 2, AQ_OP_QQMM = 3, AQ_OP_QMM_NT = 4,
+  AQ_OP_QQMM_INT8 = 5
 } aq_op;
 
 /*
@@ -356,10 +357,109 @@ AQ_API aq_status aq_qqmm(const void* x, const void* w_q, const void* scales, voi
                          size_t workspace_bytes, aq_stream_t stream);
 
 /*
+ * aq_quantize_int8 — symmetric 8-bit quantizer with one scale per row: the
+ * tokens of an activation at run time, or the channels of a weight once.  Per
+ * row, in fp32:
+ *   scales[r] = max |x| / 127 (IEEE division)
+ *   x_q = rint(x / scales[r]) (IEEE division, ties to even), in [-127, 127];
+ *   0 for a row of zeros (scale 0)
+ * Bit-exact.  A row with a NaN gets scale NaN, one with an infinity scale
+ * +inf, and codes 0, so that aq_int8_mm gives NaN for it.
+ *   x [rows, K] T, x_q [rows, K] int8, scales [rows] fp32; x and x_q 16-byte
+ *   aligned, scales 4; K a multiple of 16.
+ */
+AQ_API aq_status aq_quantize_int8(const void* x, void* x_q, float* scales, int64_t rows, int64_t K,
+                                  aq_dtype dtype, aq_stream_t stream);
+
+/*
+ * aq_int8_mm — matrix product of 8-bit integers with a scale per token and
+ * per channel (W8A8):
+ *   y[m, n] = T((float(sum_k x_q[m, k] w_q[n, k]) * x_scales[m]) * w_scales[n])
+ * The sum is exact (32-bit integers); float() rounds it once, and the two
+ * fp32 products and the cast to T round once each.
+ *   x_q [M, K], w_q [N, K] int8 (any codes, -128 included; 16-byte aligned);
+ *   x_scales [M], w_scales [N] fp32; y [M, N] T, 16-byte aligned.
+ *   K a multiple of 16, at most 131071 (so that the sum fits); M, N <= 2^30.
+ * One launch, no workspace.  aq_set_weight_prefetch applies to w_q.
+ */
+AQ_API aq_status aq_int8_mm(const void* x_q, const float* x_scales, const void* w_q,
+                            const float* w_scales, void* y, int64_t M, int64_t N, int64_t K,
+                            aq_dtype dtype, aq_stream_t stream);
+
+/*
+ * aq_qqmm_int8 — W8A8 matmul of an unquantized x: aq_quantize_int8 of x's
+ * rows into the workspace, then aq_int8_mm (two launches; the product's
+ * weight loads start while x is quantized).  x [M, K] T, 16-byte aligned; the
+ * rest as aq_int8_mm.  Workspace: aq_workspace_size(AQ_OP_QQMM_INT8, M, N, K,
+ * 8, 16, AQ_MODE_AFFINE, 1) bytes, 256-byte aligned; its first 64 KB are left
+ * as they are, so the buffer may be one that serves the other calls.
+ */
+AQ_API aq_status aq_qqmm_int8(const void* x, const void* w_q, const float* w_scales, void* y,
+                              int64_t M, int64_t N, int64_t K, aq_dtype dtype, void* workspace,
+                              size_t workspace_bytes, aq_stream_t stream);
+
+/* One stack of expert matrices: w_q [E, N, K*bits/8], scales / biases
+ * [E, N, K/group_size] (biases NULL for FP4); each 16-byte aligned. */
+typedef struct aq_moe_matrix {
+  const void* w_q;
+  const void* scales;
+  const void* biases;
+} aq_moe_matrix;
+
+/*
+ * aq_moe — a whole mixture-of-experts layer for a few tokens, in one launch
+ * (the serving step around the products that aq_gather_qmm gives for indices
+ * known on the host).  Per token x [H]:
+ *   l = x . w_router^T                 (exact products, fp64 sums)
+ *   the top_k experts by l (ties: the lower index), p = softmax(l) over all E
+ *   weight = p_e, or with `normalize` p_e / sum of the chosen p
+ *   h_e = silu(x . gate_e^T) * (x . up_e^T),   silu(v) = v / (1 + exp(-v))
+ *   y = sum over the slots, in order, of weight * (h_e . down_e^T)
+ * Weights are never rounded to T (scale and bias apply in fp32 per group, as
+ * in aq_qmv), h keeps 16 bits of significand, and each y is rounded once.
+ * Equal inputs give equal outputs.
+ *   x [T, H], w_router [E, H], y [T, H] in T, 16-byte aligned
+ *   gate, up: N = I, K = H; down: N = H, K = I (aq_moe_matrix, host structs
+ *   read before the call returns), one format for all three
+ *   indices [T, top_k] int32 and weights [T, top_k] fp32: outputs, in the
+ *   order of the logits; a NaN logit makes all weights of its token NaN.
+ * 0 <= T <= 64, 1 <= E <= 512, 1 <= top_k <= min(16, E); H and I are multiples
+ * of 32 and of group_size, at most 65536; AQ_ERR_INVALID_ARG otherwise.
+ * The kernel is launched cooperatively (its steps meet at grid barriers) and
+ * holds every SM: a call on another stream runs before or after it.
+ * Workspace: aq_moe_workspace_size bytes, under aq_qmv's rules (zero-filled
+ * before its first use; calls that may overlap need separate buffers).
+ */
+AQ_API aq_status aq_moe(const void* x, const void* w_router, const aq_moe_matrix* gate,
+                        const aq_moe_matrix* up, const aq_moe_matrix* down, void* y,
+                        int32_t* indices, float* weights, int64_t T, int64_t H, int64_t I,
+                        int64_t E, int64_t top_k, int normalize, int bits, int group_size,
+                        aq_mode mode, aq_dtype dtype, void* workspace, size_t workspace_bytes,
+                        aq_stream_t stream);
+
+/*
+ * aq_moe_experts — the experts of aq_moe for routing done elsewhere: indices
+ * [T, top_k] int32 and weights [T, top_k] fp32 are DEVICE inputs.  A slot
+ * whose index is not in 0 .. E-1 is skipped whatever its weight (padding: -1);
+ * a token without a slot gives y = 0; an expert named twice counts twice.
+ * top_k may exceed E.  Otherwise as aq_moe.
+ */
+AQ_API aq_status aq_moe_experts(const void* x, const int32_t* indices, const float* weights,
+                                const aq_moe_matrix* gate, const aq_moe_matrix* up,
+                                const aq_moe_matrix* down, void* y, int64_t T, int64_t H,
+                                int64_t I, int64_t E, int64_t top_k, int bits, int group_size,
+                                aq_mode mode, aq_dtype dtype, void* workspace,
+                                size_t workspace_bytes, aq_stream_t stream);
+
+/* Workspace bytes of aq_moe / aq_moe_experts (0 for sizes they refuse). */
+AQ_API size_t aq_moe_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
+
+/*
  * aq_workspace_size — bytes of workspace the given call needs (0 if none).
  * For AQ_OP_QCONV2D pass M = B*Ho*Wo, N = Cout / groups, K = Kp and the
  * number of conv groups in `groups`; for the others pass groups = 1 (and for
- * AQ_OP_QQMM bits = 4, mode = AQ_MODE_FP4).
+ * AQ_OP_QQMM bits = 4, mode = AQ_MODE_FP4; AQ_OP_QQMM_INT8 ignores bits,
+ * group_size and mode).
  */
 AQ_API size_t aq_workspace_size(aq_op op, int64_t M, int64_t N, int64_t K, int bits, int group_size,
                          aq_mode mode, int groups);

@@ -9,8 +9,8 @@
  * the other roles run out.  The pages have no counterpart.
  *
  * Scope: the warp-MMA decode kernel behind aq_qmv / aq_qmv_batched /
- * aq_qmv_noalloc (4-bit affine weights), aq_qmv's kernel choice, and
- * aq_gather_qmm's grouping of index pairs.  The
+ * aq_qmv_noalloc (4-bit affine weights), aq_qmv's kernel choice,
+ * aq_gather_qmm's grouping of index pairs, and aq_int8_mm's tile.  The
  * settings are process-wide and apply to launches made after the call; 0
  * restores the default.
  */
@@ -37,6 +37,12 @@ AQ_API void aq_testing_set_start_delay_ns(uint64_t ns);
  * kernel on the same shapes; the workspace that aq_workspace_size reports
  * covers every kernel. */
 AQ_API void aq_testing_set_qmv_kernel(int which);
+
+/* Tile that later aq_int8_mm / aq_qqmm_int8 calls of this process use:
+ * `tokens` per tile (16, 32, 64 or 128; 128 or 256 with `pair`, two CTAs to a
+ * tile) and at most `splits` K-slices (1..8, without `pair`).  0 tokens: the
+ * automatic choice (default). */
+AQ_API void aq_testing_set_int8_plan(int tokens, int pair, int splits);
 
 /* The expert grouping aq_gather_qmm would use for these index pairs (host
  * logic only, no launch): returns the number of grouped problems (0 when the
