@@ -6,23 +6,24 @@
 //
 // What bounds it: the packed weights of the experts chosen are read once,
 // 3 I H codes each, while a token costs only one multiply-add per code; so the
-// layer runs at the rate the weights stream from HBM, and for a token or two
-// at the latency of its dependent steps.  Hence one cooperative kernel, one
-// CTA per SM, with the steps separated by grid barriers instead of launches:
-// router products, [barrier] top-k and plan (every CTA for itself), gate/up,
-// [barrier] down, [barrier] weighted sums.  The down weights of a warp's
-// first unit are already under way while it waits at the barrier before.
+// floor is the rate the weights stream from HBM, and for a token or two the
+// latency of the dependent steps.  Hence one cooperative kernel, one CTA per
+// SM, with the steps separated by grid barriers instead of launches: router
+// products, [barrier] top-k and plan (every CTA for itself), gate/up,
+// [barrier] down, [barrier] weighted sums.  The first down weights are already
+// under way while a CTA waits at the barrier before.
 //
-// A unit of work is a 16-row tile of weights times up to 8 of the tokens that
-// chose its expert, done by one warp (or a team of warps that share K and add
-// their sums in shared memory, when there are fewer units than warps): 8 gate
-// rows and the same 8 up rows, so that a thread holds both factors of h, or
-// 16 down rows.  A warp streams its rows by cp.async through a ring of its
-// own in shared memory, so no unit waits for another warp.  The codes become
-// the A operand of mma.m16n8k16 as exact small numbers (offset integers for
-// affine codes, E2M1 values for FP4) and x the B operand; per group the
-// products P and, with an A operand of ones, the sums X of x leave in fp32:
-//   sum += s P' + (b - offset s) X,      P' = sum (offset + q) x.
+// Work is cut into row tiles of 16 rows (8 gate rows and the same 8 up rows, so
+// that both factors of h meet in one place, or 16 down rows) times a token tile,
+// up to 8 of the tokens that chose the expert.  A CTA takes neighbouring row
+// tiles; a team of 4, 8 or 16 of its warps shares the K of one, so each warp
+// keeps its part of x in registers over all row tiles of a token tile and
+// streams its part of the weight rows by cp.async through a ring of its own.
+// The warps' sums meet in shared memory after two row tiles per team.
+//
+// The codes become the A operand of mma.m16n8k16 as exact small numbers and x
+// the B operand; per group the products P and the sums X of x leave in fp32:
+//   sum += s P + b X,      P = sum (offset + q) x - offset X.
 // So w_hat is never rounded to T.  h is kept as two bf16 numbers (hi + lo, 16
 // bits of significand), in the B operand's order, so that down's operand
 // rounds far below T.  Each pair (token, slot) has its row of fp32 results;
@@ -47,6 +48,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxPairs = 1024;          // tokens * top_k
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopK = 16;
+constexpr int kExchangeLanes = 33;       // a lane more, to spread the banks
 constexpr int kCounterBytes = 65536;     // the workspace's shared counter area
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -72,91 +74,111 @@ struct Format {
   // out one by one; for groups of 16 a thread holds 4 codes of each group.
   static constexpr Order kOrder = GS == 16 ? Order::kGroup16
                                   : (BITS == 2 || BITS == 4) ? Order::kSplit : Order::kPairs;
-  static constexpr int kStageK = BITS <= 4 ? 256 : 128;   // elements of K per ring stage
-  static constexpr int kRowBytes = kStageK * BITS / 8;
-  static constexpr int kRowPitch = kRowBytes + 16;        // spreads 8 rows over the banks
   static constexpr int kScaleSize = FP4 ? 1 : 2;
-  static constexpr int kScaleBytes = kStageK / GS * kScaleSize;   // per row and stage
-  // room for the aligned 4-byte words that hold a row's scales of a stage
-  static constexpr int kScalePitch = (kScaleBytes + 4 + 7) / 8 * 8;
-  static constexpr int kSlot = 16 * kRowPitch + (FP4 ? 1 : 2) * 16 * kScalePitch;
-  static constexpr int kRingFit = 168 * 1024 / (kWarps * kSlot);
-  static constexpr int kRing = kRingFit > 8 ? 8 : kRingFit;
-  static_assert(kRing >= 3 && kSlot % 16 == 0, "ring");
+  // 32-chunks of x a warp holds with NB operands each: what the registers take,
+  // and what lets two stages of 16 warps' chunks fit the ring.
+  template <int NB> static constexpr int kHeld = BITS <= 4 ? 8 / NB : 4;
+  // A stage of a warp: its part of 16 rows.  A copied window starts at the 16
+  // bytes (codes; rows start at multiples of 4 bytes, of 16 for 4 and 8 bits)
+  // or 4 bytes (scales) below the part; pitches spread 8 rows over the banks.
+  static constexpr int kCodeBytes = kHeld<1> * 4 * BITS;
+  static constexpr int kPitch = 16 * (((kCodeBytes + (BITS == 4 || BITS == 8 ? 0 : 12) + 15) / 16) | 1);
+  static constexpr int kScaleBytes = kHeld<1> * 32 / GS * kScaleSize;
+  static constexpr int kScaleWords = (kScaleBytes + (FP4 ? 3 : 2) + 3) / 4;
+  static constexpr int kScalePitch = (kScaleWords + 1) / 2 * 8;
+  static constexpr int kSlot = 16 * kPitch + (FP4 ? 1 : 2) * 16 * kScalePitch;
+  static_assert(kPitch <= 9 * 16 && kSlot % 16 == 0, "eight lanes copy a row");
 };
 
+template <int OFF>
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(v) : "r"(a), "n"(OFF));
   return v;
 }
+template <int OFF>
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2+%3];" : "=r"(v.x), "=r"(v.y) : "r"(a), "n"(OFF));
   return v;
 }
+template <int OFF>
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a));
+  uint32_t v;
+  asm volatile("ld.shared.u16 %0, [%1+%2];" : "=r"(v) : "r"(a), "n"(OFF));
   return v;
+}
+
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f4(uint32_t a, const float4& v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+// (v & mask) | magic in one instruction, which takes one constant only: the
+// other is kept in a register.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "n"(MASK), "r"(magic));
+  return r;
 }
 
 template <typename O> struct Op;         // operand type of an mma
 template <> struct Op<__half> {
-  static constexpr uint32_t kMagic = 0x64006400u;         // 1024 + q
-  static constexpr float kOffset = 0.0f;                  // taken off again, below
+  static constexpr uint32_t kMagic = 0u;                  // q * 2^-24, a subnormal
+  static constexpr float kOffset = 0.0f;
   static constexpr uint32_t kOnes = 0x3C003C00u;
+  // d = A B + {c0, c1, c2, c3}
   static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
-        " {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                             uint32_t a3, uint32_t b0, uint32_t b1, float c0,
+                                             float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+        " {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
   }
 };
 template <> struct Op<__nv_bfloat16> {
   static constexpr uint32_t kMagic = 0x43004300u;         // 128 + q, q < 128
   static constexpr float kOffset = 128.0f;
   static constexpr uint32_t kOnes = 0x3F803F80u;
+  // d = A B + {c0, c1, c2, c3}
   static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7},"
-        " {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                             uint32_t a3, uint32_t b0, uint32_t b1, float c0,
+                                             float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+        " {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
   }
 };
 
-// What the operand holds beside the code: P' = sum (offset + q) x.  8-bit
-// codes do not fit bf16's 7 bits beside 128 and become q - 128 (exact).  With
-// fp16's 1024 the products of the offset would cost up to 9 bits of the fp32
-// sums (2-bit codes in groups of 128: 3.5e-4 instead of 2.1e-4 of error after
-// rounding to fp16), so it is subtracted from the operand, which is exact.
+// What the operand holds beside the code: P' = sum (offset + q) x.  In bf16 codes
+// of 8 bits do not fit the 7 bits beside 128 and become q - 128 (exact).
+// In fp16 the bits of a code are the subnormal q * 2^-24: no offset.
 template <typename O, typename F>
 __host__ __device__ constexpr float code_offset() {
   return F::kFp4 ? 0.0f
          : (F::kBits == 8 && std::is_same<O, __nv_bfloat16>::value) ? -128.0f : Op<O>::kOffset;
 }
-// What the operand's values are multiplied with afterwards (FP4 in fp16: the
-// code's bits are those of value * 2^-14).
+// What the operand's values are multiplied with afterwards (fp16: 2^24, or
+// 2^14 for FP4, whose code's bits are those of value * 2^-14).
 template <typename O, typename F>
 __host__ __device__ constexpr float product_scale() {
-  return F::kFp4 && std::is_same<O, __half>::value ? 16384.0f : 1.0f;
-}
-
-// The operand word of two codes under the magic exponent.
-template <typename O>
-__device__ __forceinline__ uint32_t from_magic(uint32_t v) {
-  if constexpr (std::is_same<O, __half>::value) {
-    const uint32_t k = Op<O>::kMagic;
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v),
-                              *reinterpret_cast<const __half2*>(&k));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  } else {
-    return v;
-  }
+  return !std::is_same<O, __half>::value ? 1.0f : F::kFp4 ? 16384.0f : 16777216.0f;
 }
 
 template <typename O>
@@ -174,36 +196,33 @@ __device__ __forceinline__ uint32_t e2m1_pair(uint32_t t) {   // codes in bits 0
 }
 
 // The four operand words (two mma k-steps of two words) of a thread's 8 codes
-// of one row's 32-chunk; `at` is the shared address of the row's chunk.
-template <typename O, typename F>
-__device__ __forceinline__ void operand(uint32_t at, int t, uint32_t (&r)[4]) {
-  constexpr uint32_t magic = Op<O>::kMagic;
+// of one row's 32-chunk, OFF bytes after the shared address `at`.
+template <typename O, typename F, int OFF>
+__device__ __forceinline__ void operand(uint32_t at, int t, uint32_t magic, uint32_t (&r)[4]) {
   if constexpr (F::kOrder == Order::kGroup16) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const uint32_t w = __byte_perm(lds16(at + 8 * g + 2 * t), 0u, 0x4140);
+      const uint32_t w = __byte_perm(g ? lds16<OFF + 8>(at + 2 * t) : lds16<OFF>(at + 2 * t), 0u, 0x4140);
       r[2 * g] = e2m1_pair<O>(w & 0x000F000Fu);
       r[2 * g + 1] = e2m1_pair<O>((w >> 4) & 0x000F000Fu);
     }
   } else if constexpr (F::kBits == 4) {
-    const uint32_t w = lds32(at + 4 * t);
+    const uint32_t w = lds32<OFF>(at + 4 * t);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t q = (w >> (4 * i)) & 0x000F000Fu;
-      r[i] = F::kFp4 ? e2m1_pair<O>(q) : from_magic<O>(q | magic);
-    }
+    for (int i = 0; i < 4; ++i)
+      r[i] = F::kFp4 ? e2m1_pair<O>((w >> (4 * i)) & 0x000F000Fu) : and_or<0x000F000Fu>(w >> (4 * i), magic);
   } else if constexpr (F::kBits == 2) {
-    const uint32_t w = __byte_perm(lds16(at + 2 * t), 0u, 0x4140);
+    const uint32_t w = __byte_perm(lds16<OFF>(at + 2 * t), 0u, 0x4140);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = from_magic<O>(((w >> (2 * i)) & 0x00030003u) | magic);
+    for (int i = 0; i < 4; ++i) r[i] = and_or<0x00030003u>(w >> (2 * i), magic);
   } else if constexpr (F::kBits == 8) {
-    const uint2 w = lds64(at + 8 * t);
+    const uint2 w = lds64<OFF>(at + 8 * t);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t v = i < 2 ? w.x : w.y;
       const uint32_t sel = i & 1 ? 0x4342u : 0x4140u;
       if constexpr (std::is_same<O, __half>::value) {
-        r[i] = from_magic<O>(__byte_perm(v, 0x64646464u, sel));   // 1024 + q
+        r[i] = __byte_perm(v, 0u, sel);
       } else {
         // 128 + (q & 127), minus 256 below 128 and 128 from there: q - 128
         const uint32_t q = __byte_perm(v, 0u, sel);
@@ -217,7 +236,7 @@ __device__ __forceinline__ void operand(uint32_t at, int t, uint32_t (&r)[4]) {
   } else {
     // 3, 5, 6 bits: the thread's 8 codes are BITS bytes from byte BITS * t
     const uint32_t byte = F::kBits * t;
-    const uint32_t w0 = lds32(at + (byte & ~3u)), w1 = lds32(at + (byte & ~3u) + 4);
+    const uint32_t w0 = lds32<OFF>(at + (byte & ~3u)), w1 = lds32<OFF + 4>(at + (byte & ~3u));
     const uint32_t sh = (byte & 3u) * 8u;
     const uint32_t v[2] = {__funnelshift_r(w0, w1, sh), w1 >> sh};
     constexpr uint32_t mask = (1u << F::kBits) - 1u;
@@ -229,7 +248,7 @@ __device__ __forceinline__ void operand(uint32_t at, int t, uint32_t (&r)[4]) {
         const int bit = F::kBits * (2 * i + j);
         q[j] = bit >= 32 ? v[1] >> (bit - 32) : __funnelshift_r(v[0], v[1], bit);
       }
-      r[i] = from_magic<O>((q[0] & mask) | ((q[1] & mask) << 16) | magic);
+      r[i] = (q[0] & mask) | ((q[1] & mask) << 16) | magic;
     }
   }
 }
@@ -270,15 +289,17 @@ __device__ __forceinline__ uint32_t h_offset(int kk) {
 }
 
 // ----------------------------------------------------------------- cp.async
-template <int N>
+template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() {
+// Wait until at most N of this thread's groups are under way.
+template <int N>
+__device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
@@ -291,21 +312,19 @@ struct Plan {
   int16_t tile_expert[kMaxPairs];
   int16_t tile_first[kMaxPairs];         // into order
   uint8_t tile_count[kMaxPairs];
-  int count[kMaxExperts];
-  int first[kMaxExperts];
+  int16_t count[kMaxExperts];
+  int16_t first[kMaxExperts];
   int scan[2][kWarps];
   int tiles;
+  int wide;                              // some tile has more than four pairs
   int abort;
 };
 
-template <typename F>
-struct Smem {
-  static constexpr int kPlanAt = 0;
-  static constexpr int kExchangeAt = (sizeof(Plan) + 15) / 16 * 16;
-  static constexpr int kRingAt = kExchangeAt + kWarps * 512;
-  static constexpr int kBytes = kRingAt + kWarps * F::kRing * F::kSlot;
-  static_assert(kBytes <= 227 * 1024, "shared memory budget");
-};
+// Shared memory: plan, the sums that warps exchange, the ring.
+constexpr int kExchangeAt = (int)((sizeof(Plan) + 15) / 16 * 16);
+constexpr int kExchangeBytes = 2 * 2 * kWarps * kExchangeLanes * 16;
+constexpr int kRingAt = (kExchangeAt + kExchangeBytes + 127) / 128 * 128;
+constexpr int kRingBytes = (227 * 1024 - kRingAt) / kWarps / 16 * 16;   // a warp's
 
 // Every CTA of the (cooperative, so co-resident) grid arrives; false after the
 // time limit.
@@ -326,7 +345,7 @@ __device__ __forceinline__ bool grid_barrier(unsigned* counter, unsigned ctas, i
     __threadfence();
   }
   __syncthreads();
-  return *abort == 0;
+  return *(volatile int*)abort == 0;
 }
 
 // ------------------------------------------------------------------- router
@@ -366,64 +385,72 @@ __device__ __forceinline__ unsigned long long order_key(double v) {
 
 // A warp per token: top_k logits (ties: the lowest index; NaN below all
 // numbers) and their softmax weights, into the plan (and out, by CTA 0).
-__device__ __forceinline__ void choose(const Params& p, Plan& plan, int warp, int lane) {
+// Experts per lane: PER, at least E / 32.
+template <int PER>
+__device__ __forceinline__ void choose_of(const Params& p, Plan& plan, int warp, int lane) {
   const int E = p.a.E, k = p.a.top_k;
-  constexpr int kPer = kMaxExperts / 32;
   for (int t = warp; t < p.a.T; t += kWarps) {
-    double v[kPer];
+    double v[PER];
+    unsigned long long key[PER];
     double top = -INFINITY;
     bool nan = false;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
       const int e = i * 32 + lane;
-      if (i * 32 < E && e < E) {
-        v[i] = __ldcg(p.logits + t * E + e);
-        nan |= v[i] != v[i];
-        top = fmax(top, v[i]);
-      }
+      v[i] = e < E ? __ldcg(p.logits + t * E + e) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      key[i] = i * 32 + lane < E ? order_key(v[i]) : 0ull;
+      nan |= v[i] != v[i];
+      top = fmax(top, v[i]);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmax(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     float sum = 0.0f;
+    if (!p.a.normalize) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i * 32 + lane < E) sum += expf((float)(v[i] - top));
-    if (nan) sum = NAN;
+      for (int i = 0; i < PER; ++i) sum += expf((float)(v[i] - top));
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    unsigned used = 0u;                                  // of this lane's experts
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    }
     int mine = 0;                                        // lane j holds slot j
-    float mine_w = 0.0f, chosen = 0.0f;
+    double logit = 0.0;
+#pragma unroll 1
     for (int j = 0; j < k; ++j) {
-      unsigned long long best = 0ull;
+      unsigned long long best = key[0];
+      double bv = v[0];
       int at = 0;
-      double bv = 0.0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i * 32 + lane < E && !((used >> i) & 1u)) {
-          const unsigned long long key = order_key(v[i]);
-          if (key > best) {
-            best = key;
-            at = i * 32 + lane;
-            bv = v[i];
-          }
+      for (int i = 1; i < PER; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          bv = v[i];
+          at = i;
         }
       const unsigned hi = (unsigned)(best >> 32), lo = (unsigned)best;
       const unsigned win_hi = __reduce_max_sync(0xFFFFFFFFu, hi);
       const unsigned win_lo = __reduce_max_sync(0xFFFFFFFFu, hi == win_hi ? lo : 0u);
       const bool wins = hi == win_hi && lo == win_lo;
-      const int e = (int)__reduce_min_sync(0xFFFFFFFFu, wins ? (unsigned)at : 0x7FFFFFFFu);
-      const float ex = expf((float)(__shfl_sync(0xFFFFFFFFu, bv, e & 31) - top));
-      chosen += ex;
+      const int e = (int)__reduce_min_sync(0xFFFFFFFFu, wins ? (unsigned)(at * 32 + lane) : 0x7FFFFFFFu);
+      const double l = __shfl_sync(0xFFFFFFFFu, bv, e & 31);
       if (lane == j) {
         mine = e;
-        mine_w = ex;
+        logit = l;
       }
-      if (lane == (e & 31)) used |= 1u << (e >> 5);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (e == i * 32 + lane) key[i] = 0ull;
     }
+    const float ex = lane < k ? expf((float)(logit - top)) : 0.0f;
+    if (p.a.normalize) {
+      sum = ex;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    }
+    if (__any_sync(0xFFFFFFFFu, nan)) sum = NAN;         // shows in every weight
     if (lane < k) {
-      // a NaN among the logits shows in every weight
-      const float w = sum != sum ? sum : __fdiv_rn(mine_w, p.a.normalize ? chosen : sum);
+      const float w = sum != sum ? sum : __fdiv_rn(ex, sum);
       plan.expert[t * k + lane] = (int16_t)mine;
       plan.weight[t * k + lane] = w;
       if (blockIdx.x == 0) {
@@ -432,6 +459,12 @@ __device__ __forceinline__ void choose(const Params& p, Plan& plan, int warp, in
       }
     }
   }
+}
+__device__ __forceinline__ void choose(const Params& p, Plan& plan, int warp, int lane) {
+  static_assert(kMaxExperts == 512, "experts per lane");
+  if (p.a.E <= 64) choose_of<2>(p, plan, warp, lane);
+  else if (p.a.E <= 128) choose_of<4>(p, plan, warp, lane);
+  else choose_of<16>(p, plan, warp, lane);
 }
 
 // The pairs of each expert in their order, cut into tiles of up to 8: every
@@ -483,6 +516,8 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan& plan) {
     plan.tile_count[n0 + j] = (uint8_t)min(8, c - 8 * j);
   }
   if (tid == kThreads - 1) plan.tiles = bn + sn;
+  const int wide = __syncthreads_or(c > 4);
+  if (tid == 0) plan.wide = wide;
   __syncthreads();
   for (int q = tid; q < P; q += kThreads) {
     const int e = plan.expert[q];
@@ -492,317 +527,430 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan& plan) {
 }
 
 // ------------------------------------------------------- gate/up and down
+// The row tiles of one phase in a CTA, [m, end), in batches: up to `most`
+// neighbouring row tiles of one token tile.
+struct Cursor {
+  int m, end, blocks, most;
+  int tile, rb, nb;                      // token tile, first row tile, row tiles
+  __device__ __forceinline__ Cursor(int begin, int e, int bl, int mo)
+      : m(begin), end(e), blocks(bl), most(mo) {
+    tile = begin / bl;
+    rb = begin - tile * bl;
+    size();
+  }
+  __device__ __forceinline__ void size() { nb = min(min(most, end - m), blocks - rb); }
+  __device__ __forceinline__ bool more() const { return m < end; }
+  __device__ __forceinline__ void next() {
+    m += nb;
+    rb += nb;
+    if (rb == blocks) {
+      rb = 0;
+      ++tile;
+    }
+    size();
+  }
+};
+
 // PH 1: gate and up (8 rows each) over H; PH 2: down (16 rows) over I.
 template <int PH, typename T, typename F>
 struct Phase {
   using O = typename std::conditional<PH == 1, T, __nv_bfloat16>::type;
-  static constexpr int kChunks = F::kStageK / 32;        // per stage
-  static constexpr int kDepth = 4;                       // chunks of x loaded ahead
-  static_assert(kChunks >= kDepth, "x runs at most one stage ahead");
+  static constexpr int kGu = F::kGs >= 32 ? F::kGs / 32 : 1;     // chunks per group
+  static constexpr int kParts = F::template kHeld<1> / kGu;      // groups held, at most
+  static constexpr int kArrays = F::kFp4 ? 1 : 2;
+  static constexpr float kOffset = code_offset<O, F>();
+  static constexpr float kScale = product_scale<O, F>();
+
+  static constexpr int kRows = PH == 1 ? 8 : 16;         // rows of a matrix in a row tile
+  static constexpr int kSlots = kRingBytes / F::kSlot < 6 ? kRingBytes / F::kSlot : 6;
+  static_assert(kSlots >= 3, "ring");
+  static constexpr uint32_t kBuffer = 2 * kWarps * kExchangeLanes * 16;
 
   const Params& p;
-  Plan& plan;
-  const int lane, g, t;
-  const uint32_t ring;
-  int K, blocks, stages, units;                          // row blocks per tile, stages per unit
-  int team, member, warps, ustride, unit0;               // warps of a team share a unit's K
-  int64_t row_bytes, scale_row;
-  bool vec16, vec8;
-  // the next stage to copy
-  int pu, ps;
-  uint32_t pslot;
-  int64_t prow;                                          // first row of its unit in the stack
+  const Plan& plan;
+  const uint32_t ring;                   // shared address, of the warp's
+  const int warp, lane, g, t;
+  uint32_t magic;                        // the operand's bits beside a code
+  int K, chunks, blocks, row_bytes, scale_row;
+  int held;                              // chunks of x a warp holds
+  int shift, lt, team;                   // log2 of the warps of a team, of the teams
+  int pass_chunks, passes;
+  Cursor done, ahead;                    // batch to compute, batch to copy
+  int turn;                              // batches computed
+  int apass, ai;                         // pass and row tile of the next copy
+  uint32_t at, aat;                      // slots
+  int tile;                              // whose x is held
+  int first, count;                      // its pairs
+  // what a thread does the same way in every stage
+  int from, n;                           // the warp's chunks of a pass
+  const uint8_t *csrc, *ssrc;            // what it copies: codes, scales
+  int64_t other;                         // from gate's to up's codes
+  uint32_t cdst, sdst;
+  uint32_t woff, soff;                   // row g's codes and scales in a slot
+  uint32_t own, others;                  // where it puts sums, and gets them to add
+  int jtile, jcol, jrow;                 // the sums it adds: row tile, column, row
 
-  __device__ __forceinline__ Phase(const Params& pp, Plan& pl, uint32_t r, int warp, int ln)
-      : p(pp), plan(pl), lane(ln), g(ln >> 2), t(ln & 3), ring(r) {
-    K = PH == 1 ? p.a.H : p.a.I;
-    blocks = PH == 1 ? p.a.I / 8 : p.a.H / 16;
-    stages = (K + F::kStageK - 1) / F::kStageK;
-    units = plan.tiles * blocks;
-    row_bytes = (int64_t)K * F::kBits / 8;
-    scale_row = (int64_t)(K / F::kGs) * F::kScaleSize;
-    vec16 = row_bytes % 16 == 0;
-    vec8 = F::kScaleBytes % 8 == 0 && scale_row % 8 == 0;
-    // Team size with the fewest stages one after the other (and one more per
-    // unit for its start and end).
-    const int total = (int)gridDim.x * kWarps;
-    warps = 1;
-    int best = 0x7FFFFFFF;
-    for (int s = 1; s <= 8 && s <= stages; s *= 2) {
-      const int teams = total / s;
-      const int cost = ((units + teams - 1) / teams) * ((stages + s - 1) / s + 1);
-      if (cost < best) {
-        best = cost;
-        warps = s;
-      }
+  static __device__ __forceinline__ int blocks_of(const Params& p) {
+    return PH == 1 ? p.a.I / 8 : p.a.H / 16;
+  }
+  // At most 1024 token tiles of 8192 row tiles each: the product fits 32 bits.
+  static __device__ __forceinline__ int border(const Params& p, const Plan& plan, int cta) {
+    return (int)((unsigned)(plan.tiles * blocks_of(p)) * (unsigned)cta / gridDim.x);
+  }
+  // log2 of the teams: as few warps to a team as hold K, but no more teams than
+  // pairs of row tiles.
+  static __device__ __forceinline__ int teams_of(int chunks, int held, int tiles) {
+    int lt = chunks <= 4 * held ? 2 : chunks <= 8 * held ? 1 : 0;
+    while (lt > 0 && tiles <= 1 << lt) --lt;
+    return lt;
+  }
+
+  __device__ __forceinline__ Phase(const Params& pp, const Plan& pl, uint32_t ri, uint32_t exchange,
+                                   int w, int ln, int begin, int end)
+      : p(pp), plan(pl), ring(ri), warp(w), lane(ln), g(ln >> 2), t(ln & 3),
+        K(PH == 1 ? pp.a.H : pp.a.I), chunks(K / 32), blocks(blocks_of(pp)),
+        held(PH == 2 && pl.wide ? F::template kHeld<2> : F::template kHeld<1>),
+        lt(teams_of(chunks, held, end - begin)), done(begin, end, blocks, 2 << lt), ahead(done) {
+    asm volatile("mov.b32 %0, %1;" : "=r"(magic) : "n"(Op<O>::kMagic));   // not a constant, see and_or
+    shift = 4 - lt;
+    team = warp >> shift;
+    row_bytes = chunks * 4 * F::kBits;
+    scale_row = K / F::kGs * F::kScaleSize;
+    pass_chunks = held << shift;
+    passes = (chunks + pass_chunks - 1) / pass_chunks;
+    apass = ai = turn = 0;
+    at = aat = ring;
+    tile = -1;
+    place(0, from, n);
+    {
+      // codes: eight lanes to a row, four rows at a time; scales and biases: a
+      // lane to a row of each
+      const int row = lane >> 3, srow = lane & 15, arr = F::kFp4 ? 0 : lane >> 4;
+      csrc = (PH == 2 ? p.a.down : p.a.gate).w_q + row * row_bytes + (lane & 7) * 16;
+      cdst = row * F::kPitch + (lane & 7) * 16;
+      other = PH == 1 ? p.a.up.w_q - p.a.gate.w_q : 8 * (int64_t)row_bytes;
+      const MoeMatrix& m = PH == 2 ? p.a.down : srow < 8 ? p.a.gate : p.a.up;
+      ssrc = (arr ? m.biases : m.scales) + (PH == 1 ? srow & 7 : srow) * scale_row;
+      sdst = 16 * F::kPitch + (arr * 16 + srow) * F::kScalePitch;
     }
-    team = warp / warps;
-    member = warp - team * warps;
-    unit0 = team * (int)gridDim.x + (int)blockIdx.x;
-    ustride = (int)gridDim.x * (kWarps / warps);
-    pu = unit0;
-    ps = member;
-    pslot = 0;
-    place();
-  }
-
-  __device__ __forceinline__ void place() {
-    if (pu < units) {
-      const int tile = pu / blocks, rb = pu - tile * blocks;
-      prow = (int64_t)plan.tile_expert[tile] * (PH == 1 ? p.a.I : p.a.H) + rb * (PH == 1 ? 8 : 16);
+    settle();
+    own = exchange + (warp * kExchangeLanes + lane) * 16;
+    {
+      // 64 pairs of numbers per row tile, each by 4 / teams lanes that add four
+      // warps' each
+      const int spread = 2 - lt, item = (warp << (5 - spread)) + (lane >> spread);
+      const int src = (item >> 1) & 31, part = lane & ((1 << spread) - 1);
+      jtile = item >> 6;
+      jcol = 2 * (src & 3) + (item & 1);
+      jrow = src >> 2;
+      others = exchange + (((jtile & 1) * kWarps + ((jtile >> 1) << shift) + part * 4) * kExchangeLanes + src) * 16 +
+               (item & 1) * 8;
+      if (part) jtile |= 64;             // adds, but does not store
     }
-  }
-  // Row r (0..15) of a unit whose first row is `row` in a stack of matrices.
-  static __device__ __forceinline__ int64_t row_of(int64_t row, int r) {
-    return row + (PH == 1 ? (r & 7) : r);
-  }
-  __device__ __forceinline__ const MoeMatrix& matrix(int r) const {
-    return PH == 2 ? p.a.down : r < 8 ? p.a.gate : p.a.up;
+    skip();
   }
 
-  // Start the copy of the next stage (nothing when all are under way).
+  // The warp's chunks of a pass: whole groups.
+  __device__ __forceinline__ void place(int pass, int& from_, int& n_) const {
+    const int member = warp & ((1 << shift) - 1);
+    const int left = min(pass_chunks, chunks - pass * pass_chunks);
+    const int per = ((left / kGu + (1 << shift) - 1) >> shift) * kGu;
+    from_ = member * per;
+    n_ = max(0, min(per, left - from_));
+  }
+  // Bytes from a row's start to the warp's part of it.
+  __device__ __forceinline__ int code_at(int pass, int from_) const {
+    return (pass * pass_chunks + from_) * 4 * F::kBits;
+  }
+  __device__ __forceinline__ int scale_at(int pass, int from_) const {
+    return (pass * pass_chunks + from_) * 32 / F::kGs * F::kScaleSize;
+  }
+  // Where a thread finds row g (row g + 8 starts as far into its window).
+  __device__ __forceinline__ void settle(int pass = 0) {
+    woff = g * F::kPitch + ((uint32_t)(g * row_bytes + code_at(pass, from)) & 15u);
+    soff = 16 * F::kPitch + g * F::kScalePitch + ((uint32_t)(g * scale_row + scale_at(pass, from)) & 3u);
+  }
+
+  // First row, in a stack, of a row tile.
+  __device__ __forceinline__ int row0(int tl, int rb) const {
+    return plan.tile_expert[tl] * (PH == 1 ? p.a.I : p.a.H) + rb * kRows;
+  }
+  // The team's row tiles of a batch: up to 2.
+  __device__ __forceinline__ int mine(const Cursor& c) const { return min(2, c.nb - 2 * team); }
+  __device__ __forceinline__ void skip() {
+    while (ahead.more() && mine(ahead) <= 0) ahead.next();
+  }
+
+  // Start the copies of the warp's next stage: its part of a row tile.  Rows
+  // need not be aligned: the copy takes the aligned window around a part (a
+  // stack ends on a multiple of 16 bytes).
   __device__ __forceinline__ void issue() {
-    if (pu < units) {
-      const uint32_t slot = ring + pslot * F::kSlot;
-      const int left = K - ps * F::kStageK;              // elements of this stage
-      const int bytes = (left < F::kStageK ? left : F::kStageK) * F::kBits / 8;
-      const int64_t at = (int64_t)ps * F::kRowBytes;
-      if (vec16) {
-        constexpr int kPer = F::kRowBytes / 16;
-#pragma unroll
-        for (int i = 0; i < (kPer + 1) / 2; ++i) {
-          const int q = lane + 32 * i, r = q / kPer, c = (q - r * kPer) * 16;
-          if (r < 16 && c < bytes)
-            cp_async<16>(slot + r * F::kRowPitch + c,
-                         matrix(r).w_q + row_of(prow, r) * row_bytes + at + c);
-        }
-      } else {
-        constexpr int kPer = F::kRowBytes / 4;
-#pragma unroll 4
-        for (int q = lane; q < 16 * kPer; q += 32) {
-          const int r = q / kPer, c = (q - r * kPer) * 4;
-          if (c < bytes)
-            cp_async<4>(slot + r * F::kRowPitch + c,
-                        matrix(r).w_q + row_of(prow, r) * row_bytes + at + c);
+    if (ahead.more()) {
+      int f = from, m = n;
+      if (passes > 1) place(apass, f, m);
+      const int row = row0(ahead.tile, ahead.rb + 2 * team + ai);
+      {
+        const int off = code_at(apass, f), skew = ((lane >> 3) * row_bytes + off) & 15;
+        const uint8_t* src = csrc + ((int64_t)row * row_bytes + (off - skew));
+        const uint32_t dst = aat + cdst;
+        if ((lane & 7) * 16 < skew + m * 4 * F::kBits && m > 0) {
+          cp_async<16>(dst, src);
+          cp_async<16>(dst + 4 * F::kPitch, src + 4 * row_bytes);
+          cp_async<16>(dst + 8 * F::kPitch, src + other);
+          cp_async<16>(dst + 12 * F::kPitch, src + other + 4 * row_bytes);
         }
       }
-      // scales and biases: the 4-byte words that hold this stage's, 8 bytes at
-      // a time where the rows allow it
-      const int groups = (left < F::kStageK ? left : F::kStageK) / F::kGs;
+      if (m > 0 && (!F::kFp4 || lane < 16)) {
+        const int off = scale_at(apass, f), bytes = m * 32 / F::kGs * F::kScaleSize;
+        const uint8_t* src = ssrc + ((int64_t)row * scale_row + off);
+        const uint32_t dst = aat + sdst;
+        if (F::kScaleBytes % 8 == 0 && (scale_row | off) % 8 == 0) {
 #pragma unroll
-      for (int arr = 0; arr < (F::kFp4 ? 1 : 2); ++arr) {
-        const uint32_t dst = slot + 16 * F::kRowPitch + arr * 16 * F::kScalePitch;
-        if (vec8) {
-          constexpr int kPer = F::kScaleBytes / 8 > 0 ? F::kScaleBytes / 8 : 1;
-#pragma unroll
-          for (int q = lane; q < 16 * kPer; q += 32) {
-            const int r = q / kPer, c = (q - r * kPer) * 8;
-            if (c < groups * F::kScaleSize)
-              cp_async<8>(dst + r * F::kScalePitch + c,
-                          base(matrix(r), arr) + row_of(prow, r) * scale_row +
-                              (int64_t)ps * F::kScaleBytes + c);
-          }
+          for (int u = 0; u < F::kScaleBytes; u += 8)
+            if (u < bytes) cp_async<8>(dst + u, src + u);
         } else {
-          constexpr int kPer = F::kScalePitch / 4;
-          for (int q = lane; q < 16 * kPer; q += 32) {
-            const int r = q / kPer, c = (q - r * kPer) * 4;
-            const uint8_t* first = base(matrix(r), arr) + row_of(prow, r) * scale_row +
-                                   (int64_t)ps * F::kScaleBytes;
-            const uint8_t* end = first + groups * F::kScaleSize;
-            const uint8_t* src = first - ((uintptr_t)first & 3) + c;
-            if (src < end) {
-              const int n = end - src < 4 ? (int)(end - src) : 4;   // read no byte past the row
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                               dst + r * F::kScalePitch + c),
-                           "l"(src), "r"(n)
-                           : "memory");
-            }
-          }
+          const int skew = (int)(reinterpret_cast<uintptr_t>(src) & 3);
+#pragma unroll
+          for (int u = 0; u < 4 * F::kScaleWords; u += 4)
+            if (u < skew + bytes) cp_async<4>(dst + u, src - skew + u);
         }
       }
-      pslot = pslot + 1 == F::kRing ? 0 : pslot + 1;
-      ps += warps;
-      if (ps >= stages) {
-        ps = member;
-        pu += ustride;
-        place();
+      if (++ai == mine(ahead)) {
+        ai = 0;
+        if (++apass == passes) {
+          apass = 0;
+          ahead.next();
+          skip();
+        }
       }
+      aat = next(aat);
     }
     cp_commit();
   }
-  static __device__ __forceinline__ const uint8_t* base(const MoeMatrix& m, int arr) {
-    return arr ? m.biases : m.scales;
+  __device__ __forceinline__ uint32_t next(uint32_t slot) const {
+    return slot == ring + (kSlots - 1) * F::kSlot ? ring : slot + F::kSlot;
   }
   __device__ __forceinline__ void start() {
-#pragma unroll
-    for (int i = 0; i < F::kRing - 1; ++i) issue();
+#pragma unroll 1
+    for (int i = 0; i < kSlots - 1; ++i) issue();
   }
 
-  // x (or h) of this thread's column for 32-chunk c: PH 1 one vector (8
-  // values of T), PH 2 two (hi, lo).  Columns past the tile's count are zero.
-  struct X {
-    uint4 v[PH];
-  };
-  __device__ __forceinline__ X load_x(const uint8_t* col, int c) const {
-    X r;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (PH == 1) {
-      if constexpr (F::kOrder == Order::kGroup16) {
-        uint2 a = make_uint2(0u, 0u), b = a;
-        if (col) {
-          a = __ldg(reinterpret_cast<const uint2*>(col + (int64_t)c * 64 + t * 8));
-          b = __ldg(reinterpret_cast<const uint2*>(col + (int64_t)c * 64 + 32 + t * 8));
-        }
-        r.v[0] = make_uint4(a.x, a.y, b.x, b.y);
-      } else {
-        r.v[0] = col ? __ldg(reinterpret_cast<const uint4*>(col + (int64_t)c * 64 + t * 16)) : zero;
-      }
-    } else {
-      const uint4* h = reinterpret_cast<const uint4*>(col + (int64_t)c * 128 + t * 32);
-      r.v[0] = col ? h[0] : zero;
-      r.v[1] = col ? h[1] : zero;
+  // x (or h) of this thread's column for the warp's chunks of a pass, in the
+  // operand's order, and the sums of x over each group.  h is hi + lo: with up
+  // to 4 pairs in a tile columns 0-3 hold the hi parts and 4-7 the lo parts of
+  // one operand, else hi and lo are two operands.
+  uint4 xv[F::template kHeld<PH> * PH];                       // of chunk c, operand b: c * NB + b
+  float sum[kParts][2];
+
+  template <int NB>
+  __device__ __forceinline__ void load(int chunk, int n) {
+    const uint8_t* col = nullptr;
+    const int at = PH == 2 && NB == 1 ? g & 3 : g;
+    if (at < count) {
+      const int pair = plan.order[first + at];
+      col = PH == 1 ? static_cast<const uint8_t*>(p.a.x) + (int64_t)(pair / p.a.top_k) * K * 2
+                    : p.h + (int64_t)pair * K * 4 + (NB == 1 ? (g >> 2) * 16 : 0);
     }
-    return r;
+#pragma unroll
+    for (int c = 0; c < F::template kHeld<NB>; ++c) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (col && c < n) {
+          if constexpr (PH == 1 && F::kOrder == Order::kGroup16) {
+            const uint2* q = reinterpret_cast<const uint2*>(col + (int64_t)(chunk + c) * 64) + t;
+            const uint2 lo = __ldg(q), hi = __ldg(q + 4);
+            v = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          } else if constexpr (PH == 1) {
+            v = __ldg(reinterpret_cast<const uint4*>(col + (int64_t)(chunk + c) * 64) + t);
+          } else {
+            v = __ldcg(reinterpret_cast<const uint4*>(col + (int64_t)(chunk + c) * 128) + 2 * t + b);
+          }
+        }
+        xv[c * NB + b] = v;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < F::template kHeld<NB> / kGu; ++k) {
+      float S[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = k * kGu; c < (k + 1) * kGu; ++c) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          if constexpr (PH == 1) xv[c * NB + b] = order_x<F>(xv[c * NB + b]);
+          if constexpr (!F::kFp4) {
+            const uint4& v = xv[c * NB + b];
+            constexpr uint32_t one = Op<O>::kOnes;
+            Op<O>::mma(S, one, one, one, one, v.x, v.y, S[0], S[1], S[2], S[3]);
+            Op<O>::mma(S, one, one, one, one, v.z, v.w, S[0], S[1], S[2], S[3]);
+          }
+        }
+      }
+      sum[k][0] = S[0] * (1.0f / kScale);
+      sum[k][1] = S[1] * (1.0f / kScale);
+    }
   }
 
-  __device__ __forceinline__ float scale_at(uint32_t at) const {
+  template <int OFF>
+  static __device__ __forceinline__ float scale_in(uint32_t at) {
+    uint32_t b;
     if constexpr (F::kFp4) {
-      uint32_t b;
-      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(at));
+      asm volatile("ld.shared.u8 %0, [%1+%2];" : "=r"(b) : "r"(at), "n"(OFF));
       return fp4_scale_t<T>(b, F::kGs);
     } else {
-      const uint16_t b = (uint16_t)lds16(at);
-      return TT<T>::to_f(*reinterpret_cast<const T*>(&b));
+      asm volatile("ld.shared.u16 %0, [%1+%2];" : "=r"(b) : "r"(at), "n"(OFF));
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(b << 16);
+      else return __half2float(__ushort_as_half((unsigned short)b));
     }
   }
 
-  __device__ __forceinline__ void run(float* exchange) {
-    uint32_t slot_i = 0;
-    for (int u = unit0; u < units; u += ustride) {
-      const int tile = u / blocks, rb = u - tile * blocks;
-      const int first = plan.tile_first[tile], count = plan.tile_count[tile];
-      const int64_t row0 = (int64_t)plan.tile_expert[tile] * (PH == 1 ? p.a.I : p.a.H) +
-                           rb * (PH == 1 ? 8 : 16);
-      const uint8_t* col = nullptr;
-      if (g < count) {
-        const int pair = plan.order[first + g];
-        col = PH == 1 ? static_cast<const uint8_t*>(p.a.x) + (int64_t)(pair / p.a.top_k) * K * 2
-                      : p.h + (int64_t)pair * K * 4;
+  // Sums of a row tile over the warp's N chunks (0: n of them): rows g (tot 0,
+  // 1) and g + 8 (2, 3), columns 2 t and 2 t + 1.  `w`, `s`: row g's codes and
+  // scales.
+  template <int NB, int N, int C = 0>
+  __device__ __forceinline__ void multiply(float (&tot)[4], float (&P)[4], uint32_t w, uint32_t s) {
+    constexpr int k = C / kGu, kHigh = 8 * F::kScalePitch, kBias = 16 * F::kScalePitch;
+    if constexpr (N == 0 && C % kGu == 0)
+      if (C >= n) return;
+    uint32_t lo[4], hi[4];
+    operand<O, F, C * 4 * F::kBits>(w, t, magic, lo);
+    operand<O, F, C * 4 * F::kBits + 8 * F::kPitch>(w, t, magic, hi);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint4& v = xv[C * NB + b];
+        const bool begin = b == 0 && (F::kGs == 16 || (half == 0 && C % kGu == 0));
+        // a group starts from what takes the operand's offset off again
+        const float c0 = !begin ? P[0] : kOffset == 0.0f ? 0.0f : -kOffset * sum[k][0];
+        const float c1 = !begin ? P[1] : kOffset == 0.0f ? 0.0f : -kOffset * sum[k][1];
+        Op<O>::mma(P, lo[2 * half], hi[2 * half], lo[2 * half + 1], hi[2 * half + 1],
+                   half ? v.z : v.x, half ? v.w : v.y, c0, c1, begin ? c0 : P[2], begin ? c1 : P[3]);
       }
-      const int chunks = K / 32;
-      float tot[4] = {0.f, 0.f, 0.f, 0.f};
-      X xq[kDepth];
-#pragma unroll
-      for (int c = 0; c < kDepth; ++c) {
-        const int cc = member * kChunks + c;
-        xq[c] = load_x(cc < chunks ? col : nullptr, cc);
-      }
-      for (int s = member; s < stages; s += warps) {
-        cp_wait<F::kRing - 2>();
-        __syncwarp();
-        issue();
-        const uint32_t slot = ring + slot_i * F::kSlot;
-        slot_i = slot_i + 1 == F::kRing ? 0 : slot_i + 1;
-        // scales of rows g and g + 8: their offset within the copied words
-        const int64_t so = (int64_t)s * F::kScaleBytes;
-        const uint32_t dlo = (uint32_t)((row_of(row0, g) * scale_row + so) & 3);
-        const uint32_t dhi = (uint32_t)((row_of(row0, g + 8) * scale_row + so) & 3);
-        const uint32_t slo = slot + 16 * F::kRowPitch + g * F::kScalePitch + dlo;
-        const uint32_t shi = slot + 16 * F::kRowPitch + (g + 8) * F::kScalePitch + dhi;
-        const uint32_t wlo = slot + g * F::kRowPitch, whi = slot + (g + 8) * F::kRowPitch;
-        float P[4] = {0.f, 0.f, 0.f, 0.f}, S[4] = {0.f, 0.f, 0.f, 0.f};
-        auto flush = [&](int group) {
-          const uint32_t o = group * F::kScaleSize;
-          const float sl = scale_at(slo + o), sh = scale_at(shi + o);
-          constexpr float scale = product_scale<O, F>();
-          if constexpr (scale != 1.0f) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) P[i] *= scale;
-          }
-          tot[0] = fmaf(sl, P[0], tot[0]);
-          tot[1] = fmaf(sl, P[1], tot[1]);
-          tot[2] = fmaf(sh, P[2], tot[2]);
-          tot[3] = fmaf(sh, P[3], tot[3]);
-          if constexpr (!F::kFp4) {
-            constexpr float off = code_offset<O, F>();
-            const uint32_t bo = 16 * F::kScalePitch + o;
-            const float bl = fmaf(-off, sl, scale_at(slo + bo)), bh = fmaf(-off, sh, scale_at(shi + bo));
-            tot[0] = fmaf(bl, S[0], tot[0]);
-            tot[1] = fmaf(bl, S[1], tot[1]);
-            tot[2] = fmaf(bh, S[0], tot[2]);
-            tot[3] = fmaf(bh, S[1], tot[3]);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) P[i] = S[i] = 0.0f;
-        };
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const int cc = s * kChunks + c;
-          if (cc < chunks) {
-            X x = xq[c % kDepth];
-            {
-              const int nx = c + kDepth < kChunks ? cc + kDepth
-                                                  : (s + warps) * kChunks + c + kDepth - kChunks;
-              xq[c % kDepth] = load_x(nx < chunks ? col : nullptr, nx);
-            }
-            if constexpr (PH == 1) x.v[0] = order_x<F>(x.v[0]);
-            uint32_t lo[4], hi[4];
-            operand<O, F>(wlo + c * 4 * F::kBits, t, lo);
-            operand<O, F>(whi + c * 4 * F::kBits, t, hi);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll
-              for (int v = 0; v < PH; ++v) {
-                const uint32_t b0 = half ? x.v[v].z : x.v[v].x, b1 = half ? x.v[v].w : x.v[v].y;
-                Op<O>::mma(P, lo[2 * half], hi[2 * half], lo[2 * half + 1], hi[2 * half + 1], b0, b1);
-                if constexpr (!F::kFp4)
-                  Op<O>::mma(S, Op<O>::kOnes, Op<O>::kOnes, Op<O>::kOnes, Op<O>::kOnes, b0, b1);
-              }
-              if constexpr (F::kGs == 16) flush(2 * c + half);
-            }
-            if constexpr (F::kGs >= 32) {
-              if ((c + 1) % (F::kGs / 32) == 0) flush(c / (F::kGs / 32));
-            }
-          }
+      if (F::kGs == 16 || (half == 1 && (C + 1) % kGu == 0)) {
+        constexpr int o = F::kGs == 16 ? 2 * C : k * F::kScaleSize;
+        const float sl = F::kGs == 16 && half ? scale_in<o + 1>(s) : scale_in<o>(s);
+        const float sh = F::kGs == 16 && half ? scale_in<kHigh + o + 1>(s) : scale_in<kHigh + o>(s);
+        tot[0] = fmaf(sl, P[0], tot[0]);
+        tot[1] = fmaf(sl, P[1], tot[1]);
+        tot[2] = fmaf(sh, P[2], tot[2]);
+        tot[3] = fmaf(sh, P[3], tot[3]);
+        if constexpr (!F::kFp4) {
+          const float bl = scale_in<kBias + o>(s), bh = scale_in<kBias + kHigh + o>(s);
+          tot[0] = fmaf(bl, sum[k][0], tot[0]);
+          tot[1] = fmaf(bl, sum[k][1], tot[1]);
+          tot[2] = fmaf(bh, sum[k][0], tot[2]);
+          tot[3] = fmaf(bh, sum[k][1], tot[3]);
         }
       }
-      if (warps > 1) {
-        float4* ex = reinterpret_cast<float4*>(exchange) + (team * warps) * 32;
-        if (member) ex[member * 32 + lane] = make_float4(tot[0], tot[1], tot[2], tot[3]);
-        named_barrier_sync(1 + team, 32 * warps);
-        if (member == 0)
-          for (int m = 1; m < warps; ++m) {
-            const float4 v = ex[m * 32 + lane];
-            tot[0] += v.x;
-            tot[1] += v.y;
-            tot[2] += v.z;
-            tot[3] += v.w;
-          }
-        named_barrier_sync(1 + team, 32 * warps);
-      }
-      if (member == 0) {
+    }
+    if constexpr (C + 1 < (N ? N : F::template kHeld<NB>)) multiply<NB, N, C + 1>(tot, P, w, s);
+  }
+  template <int NB>
+  __device__ __forceinline__ void products(float (&tot)[4]) {
+    constexpr int kFull = F::template kHeld<NB>, kHalf = kFull / 2;
+    const uint32_t w = at + woff, s = at + soff;
+    float P[4];
+    if (n == kFull) multiply<NB, kFull>(tot, P, w, s);
+    else if (kHalf % kGu == 0 && n == kHalf) multiply<NB, kHalf % kGu == 0 ? kHalf : kFull>(tot, P, w, s);
+    else multiply<NB, 0>(tot, P, w, s);
+  }
+
+  // The sums of a batch over the warps of each team.
+  __device__ __forceinline__ void join() {
+    const bool live = (jtile & 63) < done.nb;
+    float a = 0.0f, b = 0.0f;
+    if (live) {
+      const uint32_t o = others + (turn & 1) * kBuffer;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (2 * t + j < count) {
-            const int pair = plan.order[first + 2 * t + j];
-            if constexpr (PH == 1) {
-              const float gate = tot[j], up = tot[2 + j];
-              const float h = __fdiv_rn(gate, 1.0f + expf(-gate)) * up;
-              const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-              const float rest = h - __bfloat162float(hi);
-              // an infinity or NaN is kept by the first part alone
-              const __nv_bfloat16 lo = __float2bfloat16_rn(fabsf(rest) <= 3.0e38f ? rest : 0.0f);
-              uint8_t* dst = p.h + (int64_t)pair * p.a.I * 4 + h_offset<F>(rb * 8 + g);
-              *reinterpret_cast<__nv_bfloat16*>(dst) = hi;
-              *reinterpret_cast<__nv_bfloat16*>(dst + 16) = lo;
-            } else {
-              float* dst = p.part + (int64_t)pair * p.a.H + rb * 16 + g;
-              dst[0] = tot[j];
-              dst[8] = tot[2 + j];
-            }
+      for (int m = 0; m < 4; ++m) {
+        const float2 v = lds_f2(o + m * (kExchangeLanes * 16));
+        a += v.x;
+        b += v.y;
+      }
+    }
+    if (lt < 2) {
+      a += __shfl_xor_sync(0xFFFFFFFFu, a, 1);
+      b += __shfl_xor_sync(0xFFFFFFFFu, b, 1);
+      if (lt < 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, 2);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, 2);
+      }
+    }
+    if (PH == 2 && count <= 4) {                         // columns of hi and lo
+      a += __shfl_down_sync(0xFFFFFFFFu, a, 16 >> lt);
+      b += __shfl_down_sync(0xFFFFFFFFu, b, 16 >> lt);
+    }
+    if (jtile < done.nb && jcol < count) store(a, b, plan.order[first + jcol], done.rb + jtile, jrow);
+  }
+
+  // A pair of sums: (gate, up) of one h, or rows g and g + 8 of down's result.
+  __device__ __forceinline__ void store(float a, float b, int pair, int rb, int gg) const {
+    if constexpr (PH == 1) {
+      const float h = __fdividef(a, 1.0f + expf(-a)) * b;
+      const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+      const float rest = h - __bfloat162float(hi);
+      // an infinity or NaN is kept by the first part alone
+      const __nv_bfloat16 lo = __float2bfloat16_rn(fabsf(rest) <= 3.0e38f ? rest : 0.0f);
+      uint8_t* dst = p.h + (int64_t)pair * p.a.I * 4 + h_offset<F>(rb * 8 + gg);
+      *reinterpret_cast<__nv_bfloat16*>(dst) = hi;
+      *reinterpret_cast<__nv_bfloat16*>(dst + 16) = lo;
+    } else {
+      float* dst = p.part + (int64_t)pair * p.a.H + rb * 16 + gg;
+      dst[0] = a;
+      dst[8] = b;
+    }
+  }
+
+  // A warp waits for its own copies only, and all meet once per batch: the
+  // barrier publishes the batch's sums, and the buffer of the batch after next
+  // is written by warps past the next barrier.
+  __device__ __forceinline__ void run() {
+    while (done.more()) {
+      const int nb = mine(done);
+      for (int pass = 0; pass < passes; ++pass) {
+        if (done.tile != tile || passes > 1) {
+          tile = done.tile;
+          first = plan.tile_first[tile];
+          count = plan.tile_count[tile];
+          if (passes > 1) {
+            place(pass, from, n);
+            settle(pass);
           }
+          if (PH == 2 && count > 4) load<PH>(pass * pass_chunks + from, n);
+          else load<1>(pass * pass_chunks + from, n);
+        }
+        uint32_t to = own + (turn & 1) * kBuffer;
+        for (int i = 0; i < nb; ++i) {
+          cp_wait<kSlots - 2>();
+          __syncwarp();
+          issue();
+          float tot[4] = {0.f, 0.f, 0.f, 0.f};
+          if (PH == 2 && count > 4) products<PH>(tot);
+          else products<1>(tot);
+          at = next(at);
+          float4 v = make_float4(tot[0], tot[2], tot[1], tot[3]);
+          if constexpr (kScale != 1.0f) {
+            v.x *= kScale;
+            v.y *= kScale;
+            v.z *= kScale;
+            v.w *= kScale;
+          }
+          if (pass) {
+            const float4 o = lds_f4(to);
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
+          }
+          sts_f4(to, v);
+          to += kWarps * kExchangeLanes * 16;
         }
       }
+      __syncthreads();
+      join();
+      ++turn;
+      done.next();
     }
   }
 };
@@ -838,12 +986,12 @@ __device__ __forceinline__ void weighted_sums(const Params& p, const Plan& plan)
 
 template <typename T, typename F>
 __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ Params p) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  using S = Smem<F>;
+  extern __shared__ __align__(128) uint8_t smem[];
   Plan& plan = *reinterpret_cast<Plan*>(smem);
-  float* exchange = reinterpret_cast<float*>(smem + S::kExchangeAt);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ring = smem_u32(smem) + S::kRingAt + warp * F::kRing * F::kSlot;
+  // the shuffle tells the compiler that the warp's number is uniform
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t exchange = smem_u32(smem) + kExchangeAt;
+  const uint32_t ring = smem_u32(smem) + kRingAt + warp * kRingBytes;
   if (threadIdx.x == 0) plan.abort = 0;
 
   bool ok = true;
@@ -861,17 +1009,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   __syncthreads();
   if (ok) {
     make_plan(p, plan);
+    using Down = Phase<2, T, F>;
     {
-      Phase<1, T, F> up(p, plan, ring, warp, lane);
+      using Up = Phase<1, T, F>;
+      Up up(p, plan, ring, exchange, warp, lane, Up::border(p, plan, blockIdx.x),
+            Up::border(p, plan, blockIdx.x + 1));
       up.start();
-      up.run(exchange);
+      up.run();
     }
-    __syncwarp();
-    Phase<2, T, F> down(p, plan, ring, warp, lane);
+    Down down(p, plan, ring, exchange, warp, lane, Down::border(p, plan, blockIdx.x),
+              Down::border(p, plan, blockIdx.x + 1));
     down.start();
     ok = grid_barrier(p.bars + 1, gridDim.x, &plan.abort);
     if (ok) {
-      down.run(exchange);
+      down.run();
       ok = grid_barrier(p.bars + 2, gridDim.x, &plan.abort);
       if (ok) weighted_sums<T>(p, plan);
     }
@@ -890,21 +1041,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 // -------------------------------------------------------------------- host
 template <typename T, typename F>
 cudaError_t launch(const Params& p, int sms, cudaStream_t st) {
-  using S = Smem<F>;
   auto kern = moe_kernel<T, F>;
   static std::atomic<bool> attr_done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr_done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingAt + kWarps * kRingBytes);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = S::kBytes;
+  cfg.dynamicSmemBytes = kRingAt + kWarps * kRingBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
