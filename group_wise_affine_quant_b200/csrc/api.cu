@@ -720,9 +720,9 @@ aq_status aq_qqmm_int8(const void* x, const void* w_q, const float* w_scales, vo
   st = cuda_status(aq::launch_quantize_int8(x, x_q, x_scales, M, K, dtype, (cudaStream_t)stream),
                    "aq_qqmm_int8 quantizer launch");
   if (st != AQ_OK) return st;
-  // The product may start while the quantizer runs, and the quantizer starts
-  // only after everything before it has ended: no kernel that still runs then
-  // writes the weights, so they are read early whatever the thread's setting.
+  // The product may start while the quantizer runs, but only once everything
+  // before the quantizer has ended: no kernel that still runs then writes the
+  // weights, so they are read early whatever the thread's setting.
   return cuda_status(aq::launch_int8_mm(x_q, x_scales, w_q, w_scales, y, M, N, K, dtype, 1,
                                         (cudaStream_t)stream),
                      "aq_qqmm_int8 product launch");

@@ -7,10 +7,7 @@
 // that the products of such a row show it (NaN).  The row stays in registers
 // between the two passes up to K = 16384 (longer rows are read twice, the
 // second time from L2): 2 bytes in and 1 out per element.  The maximum is
-// taken on the 16-bit patterns without their sign (NaN > inf > finite).  The
-// division per element is replaced by a product with 1/s: r = x * fl(1/s) is
-// within 127 * 2^-22 of x / s, so rint agrees unless r is within 1e-4 of a
-// tie, and only then is the IEEE division done.
+// taken on the 16-bit patterns without their sign (NaN > inf > finite).
 //
 // Product: y[m, n] = T(((float)sum_k x_q w_q * s_x[m]) * s_w[n]).  The sum is
 // exact in 32-bit integers (K is limited so that it cannot overflow),
@@ -71,23 +68,42 @@ __device__ __forceinline__ RowScale row_scale(float amax) {
   r.inv = r.how == 1 ? __fdiv_rn(1.0f, r.s) : 0.0f;
   return r;
 }
-__device__ __forceinline__ uint32_t code_of(float x, const RowScale& r) {
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// The codes of two elements in the low bytes of two words: a quotient from the
+// rounded reciprocal, corrected by its exact remainder (Markstein 1990: the
+// result is the correctly rounded x / s).
+__device__ __forceinline__ uint32_t codes2(float2 x, const RowScale& r) {
+  uint64_t q;
   if (r.how == 2) {
-    const float v = fminf(fmaxf(__fdiv_rn(x, r.s), -127.0f), 127.0f);
-    return __float_as_uint(__fadd_rn(v, kRoundMagic));
+    q = pack2(__fdiv_rn(x.x, r.s), __fdiv_rn(x.y, r.s));
+  } else {
+    const uint64_t v = pack2(x.x, x.y), inv = pack2(r.inv, r.inv);
+    q = mul2(v, inv);
+    q = fma2(fma2(q, pack2(-r.s, -r.s), v), inv, q);
   }
-  const float v = __fmul_rn(x, r.inv);
-  float t = __fadd_rn(v, kRoundMagic);
-  if (fabsf(__fsub_rn(v, __fsub_rn(t, kRoundMagic))) > 0.4999f)
-    t = __fadd_rn(__fdiv_rn(x, r.s), kRoundMagic);
-  return __float_as_uint(t);
+  q = add2(q, pack2(kRoundMagic, kRoundMagic));
+  return __byte_perm((uint32_t)q, (uint32_t)(q >> 32), 0x0040);
 }
 template <typename T>
 __device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, const RowScale& r) {
-  const float2 a = unpack2<T>(lo), b = unpack2<T>(hi);
-  const uint32_t p = __byte_perm(code_of(a.x, r), code_of(a.y, r), 0x0040);
-  const uint32_t q = __byte_perm(code_of(b.x, r), code_of(b.y, r), 0x0040);
-  return __byte_perm(p, q, 0x5410);
+  return __byte_perm(codes2(unpack2<T>(lo), r), codes2(unpack2<T>(hi), r), 0x5410);
 }
 template <typename T>
 __device__ __forceinline__ uint4 codes16(const Vec16& v, const RowScale& r) {
@@ -102,126 +118,102 @@ __device__ __forceinline__ Vec16 load16(const uint4* row, int64_t i) {
   return v;
 }
 
-// A warp per row (K <= 512 * V): rows too short to keep a block busy.
-constexpr int kWarpRows = 8;
-template <typename T, int V>
-__global__ void __launch_bounds__(kWarpRows * 32)
-quantize_int8_warp_kernel(const uint4* __restrict__ x, uint4* __restrict__ xq,
-                          float* __restrict__ scales, int64_t rows, int nvec) {
+// WARPS warps per row (16 elements a thread keep most threads in flight: a warp
+// for rows of 2048 took 19.2 us for 8192 of them, four warps 11.4), V vectors
+// per thread; V = 0 reads the row twice (K > 16384).
+constexpr int kQuantThreads = 256;
+template <typename T, int WARPS, int V>
+__global__ void __launch_bounds__(kQuantThreads)
+quantize_int8_kernel(const uint4* __restrict__ x, uint4* __restrict__ xq, float* __restrict__ scales,
+                     int64_t rows, int nvec) {
+  pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5);
-  if (row >= rows) return;
+  __shared__ uint32_t part[kQuantThreads / 32];
+  constexpr int kRow = 32 * WARPS;                       // threads of a row
+  const int at = threadIdx.x % kRow, team = threadIdx.x / kRow;
+  const int64_t row = (int64_t)blockIdx.x * (kQuantThreads / kRow) + team;
+  const bool live = row < rows;
   const uint4* src = x + row * nvec * 2;
-  Vec16 v[V];
-  uint32_t m = 0u;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = lane + 32 * i;
-    if (c < nvec) {
-      v[i] = load16(src, c);
-      m = __vmaxu2(m, abs_max2(v[i]));
-    }
-  }
-  const RowScale r = row_scale(from_bits<T>(__reduce_max_sync(0xFFFFFFFFu, max_half(m))));
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = lane + 32 * i;
-    if (c < nvec) xq[row * nvec + c] = codes16<T>(v[i], r);
-  }
-  if (lane == 0) scales[row] = r.s;
-}
-
-// A block per row; V = 0 reads the row twice (K > 16384).
-constexpr int kRowThreads = 256;
-template <typename T, int V>
-__global__ void __launch_bounds__(kRowThreads)
-quantize_int8_row_kernel(const uint4* __restrict__ x, uint4* __restrict__ xq,
-                         float* __restrict__ scales, int nvec) {
-  pdl_launch_dependents();
-  __shared__ uint32_t part[kRowThreads / 32];
-  const int64_t row = blockIdx.x;
-  const uint4* src = x + row * nvec * 2;
-  uint4* dst = xq + row * nvec;
-  constexpr int kHeld = V > 0 ? V : 1;
-  Vec16 v[kHeld];
+  Vec16 v[V > 0 ? V : 1];
   uint32_t m = 0u;
   if constexpr (V > 0) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = threadIdx.x + kRowThreads * i;
-      if (c < nvec) {
+      const int c = at + kRow * i;
+      if (live && c < nvec) {
         v[i] = load16(src, c);
         m = __vmaxu2(m, abs_max2(v[i]));
       }
     }
   } else {
-    for (int c = threadIdx.x; c < nvec; c += kRowThreads) m = __vmaxu2(m, abs_max2(load16(src, c)));
+    for (int c = at; c < nvec; c += kRow) m = __vmaxu2(m, abs_max2(load16(src, c)));
   }
   m = __reduce_max_sync(0xFFFFFFFFu, max_half(m));
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-  __syncthreads();
-  m = 0u;
+  if constexpr (WARPS > 1) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = 0u;
 #pragma unroll
-  for (int i = 0; i < kRowThreads / 32; ++i) m = max(m, part[i]);
+    for (int i = 0; i < WARPS; ++i) m = max(m, part[team * WARPS + i]);
+  }
+  if (!live) return;
   const RowScale r = row_scale(from_bits<T>(m));
+  uint4* dst = xq + row * nvec;
   if constexpr (V > 0) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = threadIdx.x + kRowThreads * i;
+      const int c = at + kRow * i;
       if (c < nvec) dst[c] = codes16<T>(v[i], r);
     }
   } else {
-    for (int c = threadIdx.x; c < nvec; c += kRowThreads) dst[c] = codes16<T>(load16(src, c), r);
+    for (int c = at; c < nvec; c += kRow) dst[c] = codes16<T>(load16(src, c), r);
   }
-  if (threadIdx.x == 0) scales[row] = r.s;
+  if (at == 0) scales[row] = r.s;
 }
 
 template <typename T>
 cudaError_t quantize_rows(const void* x, void* xq, float* scales, int64_t rows, int64_t K,
                           cudaStream_t st) {
-  const uint4* px = static_cast<const uint4*>(x);
-  uint4* pq = static_cast<uint4*>(xq);
   const int nvec = (int)(K / 16);
-  if (nvec <= 128) {
-    const unsigned grid = (unsigned)((rows + kWarpRows - 1) / kWarpRows);
-    if (nvec <= 32)
-      quantize_int8_warp_kernel<T, 1><<<grid, kWarpRows * 32, 0, st>>>(px, pq, scales, rows, nvec);
-    else if (nvec <= 64)
-      quantize_int8_warp_kernel<T, 2><<<grid, kWarpRows * 32, 0, st>>>(px, pq, scales, rows, nvec);
-    else
-      quantize_int8_warp_kernel<T, 4><<<grid, kWarpRows * 32, 0, st>>>(px, pq, scales, rows, nvec);
-  } else {
-    const unsigned grid = (unsigned)rows;
-    if (nvec <= kRowThreads)
-      quantize_int8_row_kernel<T, 1><<<grid, kRowThreads, 0, st>>>(px, pq, scales, nvec);
-    else if (nvec <= 2 * kRowThreads)
-      quantize_int8_row_kernel<T, 2><<<grid, kRowThreads, 0, st>>>(px, pq, scales, nvec);
-    else if (nvec <= 4 * kRowThreads)
-      quantize_int8_row_kernel<T, 4><<<grid, kRowThreads, 0, st>>>(px, pq, scales, nvec);
-    else
-      quantize_int8_row_kernel<T, 0><<<grid, kRowThreads, 0, st>>>(px, pq, scales, nvec);
-  }
-  return cudaGetLastError();
+  const int warps = nvec <= 32 ? 1 : nvec <= 64 ? 2 : nvec <= 128 ? 4 : 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows * warps + 7) / 8));
+  cfg.blockDim = dim3(kQuantThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kern = warps == 1   ? quantize_int8_kernel<T, 1, 1>
+              : warps == 2 ? quantize_int8_kernel<T, 2, 1>
+              : warps == 4 ? quantize_int8_kernel<T, 4, 1>
+              : nvec <= kQuantThreads     ? quantize_int8_kernel<T, 8, 1>
+              : nvec <= 2 * kQuantThreads ? quantize_int8_kernel<T, 8, 2>
+              : nvec <= 4 * kQuantThreads ? quantize_int8_kernel<T, 8, 4>
+                                          : quantize_int8_kernel<T, 8, 0>;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<const uint4*>(x), static_cast<uint4*>(xq), scales,
+                            rows, nvec);
 }
 
 // ------------------------------------------------------------------ product
-// The weight is the MMA's A operand (128 channels per CTA) and x its B
-// operand (BN tokens), so that a few tokens still fill the MMA and a column
-// of the accumulator is a run of y.  Both operands are K-major 8-bit tiles of
-// 128 bytes per row (128-byte swizzle) that TMA brings into a ring of stages;
-// an elected lane issues tcgen05.mma kind::i8 into one of two accumulators in
-// TMEM while four epilogue warps scale and store the other.
-//   * kPair: two CTAs of a cluster share a tile of 256 channels x BN tokens
-//     (cta_group::2); each loads its 128 channels and half of the tokens.  A
-//     256 x 256 tile then costs each SM 32 KB per 128 of K instead of 48 KB,
-//     which is what bounds a single CTA's tile.
-//   * splits > 1 (few tiles): the CTAs of a cluster take slices of K, park
-//     their integer tiles in shared memory and add each other's through
-//     distributed shared memory, each CTA a share of the columns.
+// Both operands are K-major 8-bit tiles of 128 bytes per row (128-byte swizzle)
+// that TMA brings into a ring of stages; an elected lane issues tcgen05.mma
+// kind::i8 into one of two accumulators in TMEM while the epilogue warps scale and
+// store the other.
+//   * Few tokens: the weight is the MMA's A operand (128 channels per CTA) and
+//     x its B operand (BN tokens), so that a few tokens still fill the MMA.
+//     splits > 1 (few tiles): the CTAs of a cluster take slices of K, park their
+//     integer tiles in shared memory and add each other's through distributed
+//     shared memory, each CTA a share of the columns.
+//   * kPair: two CTAs of a cluster share a tile of 256 tokens x BN channels
+//     (cta_group::2), tokens as A operand; each loads its 128 tokens and half of
+//     the channels.  A 256 x 256 tile then costs each SM 32 KB per 128 of K
+//     instead of 48 KB, which is what bounds a single CTA's tile.  A thread
+//     holds a token's run of channels, which leaves through shared memory in
+//     TMA stores (rows of y of odd length: by the warps).
 constexpr int kBK = 128;                 // bytes (elements) of K per stage
 constexpr int kBM = 128;                 // channels per CTA
-constexpr int kMmThreads = 192;          // TMA warp, MMA warp, 4 epilogue warps
 
 template <int BN, bool PAIR>
 struct MmShape {
@@ -231,12 +223,18 @@ struct MmShape {
   static constexpr int kStage = kABytes + kBBytes;
   // BN <= 32 streams weights: five stages, so that two CTAs fit on an SM and
   // one's start and end overlap the other's stream.
-  static constexpr int kStages = BN <= 32 ? 5 : (192 * 1024) / kStage > 8 ? 8 : (192 * 1024) / kStage;
+  static constexpr int kStages = BN <= 32 ? 5 : (192 * 1024) / kStage > 8 ? 8 : PAIR && BN == 256 ? 5 : (192 * 1024) / kStage;
   static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
   static constexpr int kBars = 2 * kStages + 5;
-  static constexpr int kTail = 2 * BN * 4 + kBars * 8 + 16;     // token scales, barriers, slots
-  static constexpr int kSmem = 1024 + kStages * kStage + kTail;
-  static_assert(kStages * kStage >= BN * kBM * 4, "split-K parking reuses the ring");
+  // A quarter of the accumulator's rows to a warp, kPair: to two warps, half of
+  // the columns each (4096 x 4096 x 1024 in tiles of 256 x 128: 21.0 us, with
+  // four warps 22.4; in tiles of 256 x 256 18.6 and 18.9).
+  static constexpr int kEpilogue = PAIR ? 8 : 4;
+  static constexpr int kThreads = 64 + 32 * kEpilogue;           // TMA warp, MMA warp, epilogue
+  static constexpr int kOut = PAIR ? kEpilogue * 4096 : 0;       // staged rows of y
+  static constexpr int kTail = 2 * BN * 4 + kBars * 8 + 16;     // column scales, barriers, slots
+  static constexpr int kSmem = 1024 + kStages * kStage + kOut + kTail;
+  static_assert(PAIR || kStages * kStage >= BN * kBM * 4, "split-K parking reuses the ring");
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
@@ -249,6 +247,7 @@ struct MmArgs {
   int splits, kb_split;  // K-slices and 128-blocks per slice
   int m_tiles, n_tiles;
   int prefetch;          // weights may be read before the previous kernel has ended
+  int tma_out;           // y's rows suit TMA (N a multiple of 8)
 };
 
 __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -285,6 +284,21 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(c0), "r"(c1)
       : "memory");
 }
+// Tile store from shared memory; its rows outside the map are dropped.
+__device__ __forceinline__ void tma_store_2d(uint32_t src, const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Until the sources of all but this thread's last N store groups are read.
+template <int N> __device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
                "r"(ncols)
@@ -314,15 +328,15 @@ __device__ __forceinline__ void tile_at(int t, int m_tiles, int n_tiles, int& mt
 }
 
 template <typename T, int BN, bool PAIR>
-__global__ void __launch_bounds__(kMmThreads)
+__global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads)
 int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
-               const MmArgs a) {
+               const __grid_constant__ CUtensorMap my, const MmArgs a) {
   using S = MmShape<BN, PAIR>;
   constexpr int ST = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* tail = smem_raw + (base - raw) + ST * S::kStage;
+  uint8_t* tail = smem_raw + (base - raw) + ST * S::kStage + S::kOut;
   float* sx = reinterpret_cast<float*>(tail);                         // [2][BN]
   const uint32_t bars = smem_u32(tail + 2 * BN * 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 2 * BN * 4 + S::kBars * 8);
@@ -346,12 +360,13 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), PAIR ? 8 : 4);
+      mbar_init(tempty(b), PAIR ? 2 * S::kEpilogue : S::kEpilogue);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
     prefetch_tensormap(&mw);
     prefetch_tensormap(&mx);
+    if (PAIR && a.tma_out) prefetch_tensormap(&my);
   }
   if (warp == 1) {
     if constexpr (PAIR) tmem_alloc_pair(smem_u32(tmem_slot), S::kTmemCols);
@@ -372,7 +387,7 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
   const int tiles = a.m_tiles * a.n_tiles;
   const int kb0 = PAIR ? 0 : (int)rank * a.kb_split;
   const int nkb = PAIR ? a.kblocks : min(a.kb_split, a.kblocks - kb0);   // > 0 by the plan
-  constexpr int kChannels = PAIR ? 2 * kBM : kBM;        // channels per tile
+  constexpr int kRowsA = PAIR ? 2 * kBM : kBM;           // rows of the A operand per tile
 
   if (warp == 0) {
     // ------------------------------------------------------------- TMA warp
@@ -381,15 +396,16 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
     int pre = 0;                                         // stages whose weights are under way
     auto load_w = [&](int s, int nt, int kb) {
       const uint32_t dst = base + s * S::kStage;
-      const int row = nt * kChannels + (PAIR ? (int)rank * kBM : 0);
-      if constexpr (PAIR) tma_load_2d_pair(dst, &mw, mapa_shared(full(s), 0), kb * kBK, row);
-      else tma_load_2d(dst, &mw, full(s), kb * kBK, row);
+      if constexpr (PAIR)
+        tma_load_2d_pair(dst + S::kABytes, &mw, mapa_shared(full(s), 0), kb * kBK,
+                         nt * BN + (int)rank * S::kBRows);
+      else tma_load_2d(dst, &mw, full(s), kb * kBK, nt * kBM);
     };
     auto load_x = [&](int s, int mt, int kb) {
-      const uint32_t dst = base + s * S::kStage + S::kABytes;
-      const int row = mt * BN + (PAIR ? (int)rank * S::kBRows : 0);
-      if constexpr (PAIR) tma_load_2d_pair(dst, &mx, mapa_shared(full(s), 0), kb * kBK, row);
-      else tma_load_2d(dst, &mx, full(s), kb * kBK, row);
+      const uint32_t dst = base + s * S::kStage;
+      if constexpr (PAIR)
+        tma_load_2d_pair(dst, &mx, mapa_shared(full(s), 0), kb * kBK, mt * kRowsA + (int)rank * kBM);
+      else tma_load_2d(dst + S::kABytes, &mx, full(s), kb * kBK, mt * BN);
     };
     const uint32_t bytes = (PAIR ? 2u : 1u) * S::kStage;
     if (a.prefetch && first < tiles) {
@@ -437,7 +453,7 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA warp
     if (leader) {
-      constexpr uint32_t idesc = idesc_i8(kChannels, BN);
+      constexpr uint32_t idesc = idesc_i8(kRowsA, BN);
       uint32_t it = 0, tile_i = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step, ++tile_i) {
@@ -489,7 +505,8 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
     // ------------------------------------------------------- epilogue warps
     pdl_wait();
     const int q = warp & 3;                              // TMEM lane quarter
-    const int et = (int)threadIdx.x - 64;                // 0..127
+    constexpr int kEt = 32 * S::kEpilogue;
+    const int et = (int)threadIdx.x - 64;                // 0..kEt - 1
     T* y = static_cast<T*>(a.y);
     uint32_t tile_i = 0;
     bool ok = true;
@@ -497,48 +514,122 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
       int mt, nt;
       tile_at(t, a.m_tiles, a.n_tiles, mt, nt);
       const int b = (int)(tile_i & 1u);
-      const int m0 = mt * BN;
-      const int n = nt * kChannels + (PAIR ? (int)rank * kBM : 0) + q * 32 + lane;
-      float* sxb = sx + b * BN;
-      for (int i = et; i < BN; i += 128) sxb[i] = m0 + i < a.M ? a.xs[m0 + i] : 0.0f;
-      const float sw = n < a.N ? a.ws[n] : 0.0f;
-      named_barrier_sync(1, 128);
+      float* sxb = sx + b * BN;                          // scales of the columns
+      if constexpr (PAIR) {
+        for (int i = et; i < BN; i += kEt) sxb[i] = nt * BN + i < a.N ? a.ws[nt * BN + i] : 0.0f;
+      } else {
+        for (int i = et; i < BN; i += kEt) sxb[i] = mt * BN + i < a.M ? a.xs[mt * BN + i] : 0.0f;
+      }
+      named_barrier_sync(1, kEt);
       // after giving up the warps still meet at the barrier above
       if (ok) ok = mbar_wait(tfull(b), (tile_i >> 1) & 1u, abort_flag);
       if (!ok) continue;
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN);
-      constexpr int kCols = BN < 32 ? BN : 32;
+      if constexpr (PAIR) {
+        const int row0 = mt * kRowsA + (int)rank * kBM + q * 32;   // the warp's tokens
+        const float sm = row0 + lane < a.M ? a.xs[row0 + lane] : 0.0f;
+        uint8_t* out = smem_raw + (base - raw) + ST * S::kStage + (warp - 2) * 4096;
+        const int end = (warp - 2) / 4 * (BN / 2) + BN / 2;
 #pragma unroll 1
-      for (int c0 = 0; c0 < BN; c0 += kCols) {
-        uint32_t r[kCols];
-        if constexpr (kCols == 32) tmem_ld_32(d + c0, r);
-        else tmem_ld_16(d + c0, r);
-        tmem_ld_wait();
-        if (PAIR || a.splits == 1) {
-          if (n < a.N) {
-            T* out = y + (int64_t)(m0 + c0) * a.N + n;
-            const int cols = min(kCols, a.M - m0 - c0);
+        for (int c0 = end - BN / 2; c0 < end; c0 += 64) {
+          if (lane == 0) bulk_wait_read<0>();            // the last store has left
+          __syncwarp();
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-              if (c < cols)
-                out[(int64_t)c * a.N] =
-                    TT<T>::from_f(__fmul_rn(__fmul_rn(__int2float_rn((int)r[c]), sxb[c0 + c]), sw));
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tmem_ld_32(d + c0 + 32 * h, r);
+            float4 sc[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sc[i] = *reinterpret_cast<const float4*>(sxb + c0 + 32 * h + 4 * i);
+            tmem_ld_wait();
+            auto v = [&](int c, float w) {
+              return TT<T>::from_f(__fmul_rn(__fmul_rn(__int2float_rn((int)r[c]), sm), w));
+            };
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              T o[8];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float4 w = sc[2 * u + i];
+                o[4 * i] = v(8 * u + 4 * i, w.x);
+                o[4 * i + 1] = v(8 * u + 4 * i + 1, w.y);
+                o[4 * i + 2] = v(8 * u + 4 * i + 2, w.z);
+                o[4 * i + 3] = v(8 * u + 4 * i + 3, w.w);
+              }
+              // 128-byte rows, 16-byte units swizzled by the row
+              *reinterpret_cast<uint4*>(out + lane * 128 + (((4 * h + u) ^ (lane & 7)) * 16)) =
+                  *reinterpret_cast<const uint4*>(o);
             }
           }
-        } else {
-          int* park = reinterpret_cast<int*>(smem_raw + (base - raw));
+          if (c0 + 64 >= end) {                          // the accumulator is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(mapa_shared(tempty(b), 0));
+          }
+          const int n0 = nt * BN + c0;
+          if (a.tma_out) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (row0 < a.M && n0 < a.N) tma_store_2d(smem_u32(out), &my, n0, row0);
+              bulk_commit();
+            }
+          } else {
+            __syncwarp();
+            const int rows = min(32, a.M - row0);
+            for (int r = 0; r < rows; ++r) {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) park[(c0 + c) * kBM + q * 32 + lane] = (int)r[c];
+              for (int i = 0; i < 2; ++i) {
+                const int c = 32 * i + lane;
+                if (n0 + c < a.N)
+                  y[(int64_t)(row0 + r) * a.N + n0 + c] = *reinterpret_cast<const T*>(
+                      out + r * 128 + (((c >> 3) ^ (r & 7)) * 16) + (c & 7) * 2);
+              }
+            }
+          }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR) mbar_arrive_remote(mapa_shared(tempty(b), 0));
-        else mbar_arrive(tempty(b));
+      } else {
+        const int m0 = mt * BN;
+        const int n = nt * kBM + q * 32 + lane;
+        const float sw = n < a.N ? a.ws[n] : 0.0f;
+        constexpr int kCols = BN < 32 ? BN : 32;
+#pragma unroll 1
+        for (int c0 = 0; c0 < BN; c0 += kCols) {
+          uint32_t r[kCols];
+          if constexpr (kCols == 32) tmem_ld_32(d + c0, r);
+          else tmem_ld_16(d + c0, r);
+          if (a.splits == 1) {
+            // all scales before the first store, which the compiler takes for
+            // one that might change them
+            float4 sc[kCols / 4];
+#pragma unroll
+            for (int i = 0; i < kCols / 4; ++i) sc[i] = *reinterpret_cast<const float4*>(sxb + c0 + 4 * i);
+            tmem_ld_wait();
+            if (n < a.N) {
+              T* out = y + (int64_t)(m0 + c0) * a.N + n;
+              const int cols = min(kCols, a.M - m0 - c0);
+#pragma unroll
+              for (int c = 0; c < kCols; ++c) {
+                const float4 v = sc[c / 4];
+                const float s = c % 4 == 0 ? v.x : c % 4 == 1 ? v.y : c % 4 == 2 ? v.z : v.w;
+                if (c < cols)
+                  out[(int64_t)c * a.N] = TT<T>::from_f(__fmul_rn(__fmul_rn(__int2float_rn((int)r[c]), s), sw));
+              }
+            }
+          } else {
+            tmem_ld_wait();
+            int* park = reinterpret_cast<int*>(smem_raw + (base - raw));
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) park[(c0 + c) * kBM + q * 32 + lane] = (int)r[c];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty(b));
       }
     }
+    if (PAIR && lane == 0) bulk_wait_all();              // y is written, the buffers are free
   }
 
   if (!PAIR && a.splits > 1) {
@@ -549,21 +640,43 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
     if (warp >= 2 && *abort_flag == 0) {
       int mt, nt;
       tile_at(first, a.m_tiles, a.n_tiles, mt, nt);
-      const int row = (int)threadIdx.x - 64;
-      const int n = nt * kBM + row;
+      // a warp per column, four channels to a lane: all slices' loads of a
+      // column are under way at once
       int* park = reinterpret_cast<int*>(smem_raw + (base - raw));
-      const float sw = n < a.N ? a.ws[n] : 0.0f;
       T* y = static_cast<T*>(a.y);
+      const int n = nt * kBM + lane * 4;
+      float sw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sw[i] = n + i < a.N ? a.ws[n + i] : 0.0f;
       const int per = (BN + a.splits - 1) / a.splits;
       const int m0 = mt * BN;
       const int c_end = min(min((int)(rank + 1) * per, BN), a.M - m0);
-      for (int c = (int)rank * per; c < c_end; ++c) {
-        int sum = 0;
-        for (int r = 0; r < a.splits; ++r)
-          sum += *cluster.map_shared_rank(park + c * kBM + row, r);
-        if (n < a.N)
-          y[(int64_t)(m0 + c) * a.N + n] =
-              TT<T>::from_f(__fmul_rn(__fmul_rn(__int2float_rn(sum), sx[c]), sw));
+      for (int c = (int)rank * per + warp - 2; c < c_end; c += 4) {
+        int4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          v[r] = r < a.splits ? *reinterpret_cast<const int4*>(cluster.map_shared_rank(park + c * kBM + lane * 4, r))
+                              : make_int4(0, 0, 0, 0);
+        int sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          sum[0] += v[r].x;
+          sum[1] += v[r].y;
+          sum[2] += v[r].z;
+          sum[3] += v[r].w;
+        }
+        T o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o[i] = TT<T>::from_f(__fmul_rn(__fmul_rn(__int2float_rn(sum[i]), sx[c]), sw[i]));
+        T* out = y + (int64_t)(m0 + c) * a.N + n;
+        if (a.N % 4 == 0 && n < a.N) {
+          *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + i < a.N) out[i] = o[i];
+        }
       }
     }
     cluster.sync();
@@ -601,18 +714,19 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Rows of K bytes, boxes of 128 bytes x box_rows, 128-byte swizzle, zero fill.
-cudaError_t code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int box_rows) {
+// Rows of `row` elements, boxes of 128 bytes x box_rows, 128-byte swizzle, zero
+// fill.
+cudaError_t tile_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base,
+                     int64_t rows, int64_t row, int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
-  cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)K};
-  cuuint32_t box[2] = {kBK, (cuuint32_t)box_rows};
+  cuuint64_t dims[2] = {(cuuint64_t)row, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(row * size)};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
-                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = enc(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -630,18 +744,22 @@ cudaError_t launch_mm(const Int8Plan& p, const void* x_q, const void* w_q, MmArg
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev].store(true, std::memory_order_release);
   }
-  CUtensorMap mw, mx;
-  e = code_map(&mw, w_q, a.N, a.K, kBM);
-  if (e == cudaSuccess) e = code_map(&mx, x_q, a.M, a.K, S::kBRows);
+  CUtensorMap mw, mx, my{};
+  e = tile_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w_q, a.N, a.K, PAIR ? S::kBRows : kBM);
+  if (e == cudaSuccess)
+    e = tile_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x_q, a.M, a.K, PAIR ? kBM : BN);
+  a.tma_out = PAIR && a.N % 8 == 0;
+  if (e == cudaSuccess && a.tma_out)
+    e = tile_map(&my, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.y, a.M, a.N, 32);
   if (e != cudaSuccess) return e;
   a.splits = p.splits;
   a.kb_split = p.kb_split;
-  a.m_tiles = (a.M + BN - 1) / BN;
-  a.n_tiles = (int)((a.N + (PAIR ? 2 * kBM : kBM) - 1) / (PAIR ? 2 * kBM : kBM));
+  a.m_tiles = (a.M + (PAIR ? 2 * kBM : BN) - 1) / (PAIR ? 2 * kBM : BN);
+  a.n_tiles = (a.N + (PAIR ? BN : kBM) - 1) / (PAIR ? BN : kBM);
   const int group = PAIR ? 2 : p.splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.groups * group), 1, 1);
-  cfg.blockDim = dim3(kMmThreads, 1, 1);
+  cfg.blockDim = dim3(S::kThreads, 1, 1);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -653,7 +771,7 @@ cudaError_t launch_mm(const Int8Plan& p, const void* x_q, const void* w_q, MmArg
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = group > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, mw, mx, a);
+  return cudaLaunchKernelEx(&cfg, kern, mw, mx, my, a);
 }
 
 template <typename T>
@@ -675,41 +793,52 @@ std::atomic<int> g_force_bn{0}, g_force_pair{0}, g_force_splits{0};
 
 }  // namespace
 
-// Tile and split with the least estimated time, in clocks of one SM.  A stage
-// of 128 of K costs the larger of its MMAs (tokens * 2: 8192 multiply-adds
-// per clock) and its load from L2 (about 50 bytes per clock); a tile's start
-// and end cost about 2500, its stores 8 per column, a split's exchange 1500.
+// Tile and split with the least estimated time, in clocks of one SM, from a fit
+// to 16 shapes (1 x 2048 x 2048 to 8192 x 8192 x 2048) of all plans: a
+// 128-element block of K costs what its loads take (a few bytes per clock less
+// when every SM loads), a CTA of its own what its start and end take, and the
+// stores of a tile hide behind the next one's products if those take longer.
+// Clusters do not fill the GPU: `slots` is how many run at once.
 Int8Plan plan_int8_mm(int64_t M, int64_t N, int64_t K) {
-  const int kSms = 148;
+  struct Tile {
+    int bn;
+    bool pair;
+    int block, full, start, column;      // clocks: per block, more at full load, start, per column
+  };
+  static const Tile kTiles[6] = {{16, false, 458, 135, 4366, 90},  {32, false, 462, 160, 4800, 90},
+                                 {64, false, 469, 55, 6200, 90},   {128, false, 502, 134, 8700, 90},
+                                 {128, true, 389, 65, 6750, 14},   {256, true, 500, 130, 8500, 14}};
+  static const int kSlotsTwo[9] = {0, 296, 148, 93, 71, 56, 45, 37, 33};   // two CTAs on an SM
+  static const int kSlotsOne[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
   Int8Plan best{};
   double best_cost = 0;
   const int kblocks = (int)((K + kBK - 1) / kBK);
   const int fbn = g_force_bn.load(std::memory_order_relaxed);
   const int fpair = g_force_pair.load(std::memory_order_relaxed);
   const int fsplit = g_force_splits.load(std::memory_order_relaxed);
-  for (int c = 0; c < 6; ++c) {
-    const int bn = c < 4 ? 16 << c : 128 << (c - 4);
-    const bool pair = c >= 4;
-    if (fbn && (bn != fbn || pair != (fpair != 0))) continue;
-    const int64_t chan = pair ? 2 * kBM : kBM;
-    const int64_t tiles = ((M + bn - 1) / bn) * ((N + chan - 1) / chan);
-    const int slots = pair ? kSms / 2 : bn <= 32 ? 2 * kSms : kSms;
-    for (int s = 1; s <= (pair ? 1 : 8) && s <= kblocks; ++s) {
-      if (s > 1 && (fsplit ? s > fsplit : tiles * s > slots)) break;
+  for (const Tile& t : kTiles) {
+    if (fbn && (t.bn != fbn || t.pair != (fpair != 0))) continue;
+    const int64_t tm = t.pair ? 2 * kBM : t.bn, tn = t.pair ? t.bn : kBM;
+    const int64_t tiles = ((M + tm - 1) / tm) * ((N + tn - 1) / tn);
+    const double columns = t.pair ? (double)t.bn : (double)(M < t.bn ? M : t.bn);
+    for (int s = 1; s <= (t.pair ? 1 : 8) && s <= kblocks; ++s) {
+      const int slots = t.pair ? 74 : t.bn <= 32 ? kSlotsTwo[s] : kSlotsOne[s];
+      if (s > 1 && (fsplit ? s > fsplit : tiles > slots)) break;
       const int kb = (kblocks + s - 1) / s;
       if ((kblocks + kb - 1) / kb != s) continue;        // an empty slice
-      const double mma = 2.0 * (bn < 64 ? 64 : bn);
-      const double load = (128.0 + (pair ? bn / 2 : bn)) * kBK / 50.0 * (bn <= 32 ? 2 : 1);
-      const double waves = (double)((tiles * s + slots - 1) / slots);
-      const double cost = waves * kb * (mma > load ? mma : load) + 2500.0 + 8.0 * bn +
-                          (s > 1 ? 1500.0 : 0.0);
+      const double waves = (double)((tiles + slots - 1) / slots);
+      const double load = tiles < slots ? (double)tiles / slots : 1.0;
+      const double products = kb * (t.block + t.full * load), stores = t.column * columns * load;
+      const double cost = waves * (products > stores ? products : stores) +
+                          (s > 1 ? 5400.0 + 10.0 * t.bn + 30.0 * columns + 150.0 * s
+                                 : t.start + (t.pair ? 0.0 : 25.0 * columns));
       if (best.bn == 0 || cost < best_cost || fsplit) {
         best_cost = cost;
-        best.bn = bn;
-        best.pair = pair;
+        best.bn = t.bn;
+        best.pair = t.pair;
         best.splits = s;
         best.kb_split = kb;
-        best.groups = s > 1 ? tiles : (tiles < slots ? tiles : slots);
+        best.groups = s > 1 || tiles < slots ? tiles : slots;
       }
     }
   }
