@@ -77,7 +77,7 @@ class MoeMatrix(ctypes.Structure):
     _fields_ = [("w_q", _P), ("scales", _P), ("biases", _P)]
 
 
-_MM = ctypes.POINTER(MoeMatrix)
+MoeMatrixPtr = _MM = ctypes.POINTER(MoeMatrix)
 SIGNATURES["aq_moe"] = (_I, [_P, _P, _MM, _MM, _MM, _P, _P, _P] + [_I64] * 5 +
                         [_I, _I, _I, _I, _I, _P, _SZ, _P])
 SIGNATURES["aq_moe_experts"] = (_I, [_P, _P, _P, _MM, _MM, _MM, _P] + [_I64] * 5 +

@@ -9,6 +9,8 @@ W8A8 functions take int8 codes and fp32 scales; the mixture-of-experts ones
 take stacks [E, ...] of the same weights.
 """
 import contextlib
+import ctypes
+import functools
 
 import torch
 
@@ -36,8 +38,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# torch.cuda.current_stream builds an object for each call (2.3 us of a call's
+# 10); the handle alone takes 0.1.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    if _raw_stream is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def _mode(scales):
@@ -290,23 +299,27 @@ def aq_qconv2d_nhwc(x, w_q, scales, biases, Cout, kh, kw, stride=(1, 1), pad=(0,
     return out
 
 
-def _tensor(name, t, dtype, *shape):
-    """Refuse a tensor the C call cannot take as it is (it sees only the address)."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+def _fits(t, dtype, shape, dev):
+    """Whether the C call can take the tensor as it is (it sees only the address)."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
 
 
-def _same_device(x, *others):
-    for t in others:
-        if t is not None and t.device != x.device:
+def _refuse(x, *checks):
+    """Raise what is wrong with the first (name, tensor, dtype, shape) that does not fit."""
+    for name, t, dtype, shape in checks:
+        if not t.is_cuda:
+            if x.is_cuda:
+                raise ValueError("all tensors must be on one device, got %s and %s" % (x.device, t.device))
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if t.device != x.device:
             raise ValueError("all tensors must be on one device, got %s and %s" % (x.device, t.device))
+        if t.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    raise ValueError("tensors on %s" % x.device)
 
 
 def _matrix_shape(name, t):
@@ -318,25 +331,64 @@ def _matrix_shape(name, t):
 _no_guard = contextlib.nullcontext()
 
 
-def _on(device):
-    """Make `device` the current one for a launch."""
-    return _no_guard if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _on(dev):
+    """Make device number `dev` the current one for a launch."""
+    return _no_guard if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+_scratch = {}
+
+
+def _workspace(workspace, x, nbytes, stream, counters):
+    """The caller's Workspace, or a buffer of this device and stream (calls on
+    two streams may overlap); a call that is being captured gets one of its
+    own, which lives in the graph's memory."""
+    if workspace is not None:
+        return workspace.get(x.device, nbytes)
+    if torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        if counters:
+            buf[:_COUNTER_BYTES].zero_()
+        return buf
+    key = (x.get_device(), stream)
+    buf = _scratch.get(key)
+    if buf is None or buf.numel() < nbytes:
+        buf = _scratch[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=x.device)
+    return buf
+
+
+_COUNTER_BYTES = 65536           # at a workspace's start, zero between calls (include/aq.h)
+
+
+@functools.lru_cache(maxsize=4096)
+def _qqmm_int8_bytes(M, N, K):
+    return lib().aq_workspace_size(AQ_OP_QQMM_INT8, M, N, K, 8, 16, AQ_MODE_AFFINE, 1)
+
+
+@functools.lru_cache(maxsize=4096)
+def _moe_bytes(T, H, I, E, k):
+    return lib().aq_moe_workspace_size(T, H, I, E, k)
 
 
 def aq_quantize_int8(x, out=None):
     """x [R, K] fp16/bf16 -> (codes int8 [R, K], scales fp32 [R]): a symmetric
     scale per row (a token, or a channel of a weight)."""
-    R, K = _matrix_shape("x", x)
-    dt = _dt(x)
+    shape = _matrix_shape("x", x)
+    dt, dev = _dt(x), x.get_device()
+    R, K = shape
+    if dev < 0 or not x.is_contiguous():
+        _refuse(x, ("x", x, x.dtype, shape))
     if out is None:
-        out = (torch.empty((R, K), dtype=torch.int8, device=x.device),
-               torch.empty((R,), dtype=torch.float32, device=x.device))
-    _same_device(x, *out)
-    px = _tensor("x", x, x.dtype, R, K)
-    pq, ps = _tensor("codes", out[0], torch.int8, R, K), _tensor("scales", out[1], torch.float32, R)
-    with _on(x.device):
-        check(lib().aq_quantize_int8(px, pq, ps, R, K, dt, _stream(x.device)), "aq_quantize_int8")
-    return out
+        q, s = torch.empty_like(x, dtype=torch.int8), x.new_empty((R,), dtype=torch.float32)
+    else:
+        q, s = out
+        if not (_fits(q, torch.int8, shape, dev) and _fits(s, torch.float32, (R,), dev)):
+            _refuse(x, ("codes", q, torch.int8, shape), ("scales", s, torch.float32, (R,)))
+    with _on(dev):
+        st = lib().aq_quantize_int8(x.data_ptr(), q.data_ptr(), s.data_ptr(), R, K, dt, _stream(x.device))
+    if st:
+        check(st, "aq_quantize_int8")
+    return q, s
 
 
 def aq_int8_mm(x_q, x_scales, w_q, w_scales, dtype=torch.bfloat16, out=None):
@@ -344,15 +396,26 @@ def aq_int8_mm(x_q, x_scales, w_q, w_scales, dtype=torch.bfloat16, out=None):
     int8 x_q [M, K], w_q [N, K] and fp32 scales per token and channel."""
     M, K = _matrix_shape("x_q", x_q)
     N = _matrix_shape("w_q", w_q)[0]
+    dev = x_q.get_device()
+    if out is not None:
+        dtype = out.dtype
+    dt = _DT.get(dtype)
+    if dt is None:
+        raise TypeError("expected fp16 or bf16 as the result's type, got %s" % dtype)
+    i8, f32 = torch.int8, torch.float32
+    if not (dev >= 0 and _fits(x_q, i8, (M, K), dev) and _fits(w_q, i8, (N, K), dev)
+            and _fits(x_scales, f32, (M,), dev) and _fits(w_scales, f32, (N,), dev)):
+        _refuse(x_q, ("x_q", x_q, i8, (M, K)), ("x_scales", x_scales, f32, (M,)),
+                ("w_q", w_q, i8, (N, K)), ("w_scales", w_scales, f32, (N,)))
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=x_q.device)
-    dt = _dt(out)
-    _same_device(x_q, x_scales, w_q, w_scales, out)
-    px, pxs = _tensor("x_q", x_q, torch.int8, M, K), _tensor("x_scales", x_scales, torch.float32, M)
-    pw, pws = _tensor("w_q", w_q, torch.int8, N, K), _tensor("w_scales", w_scales, torch.float32, N)
-    py = _tensor("out", out, out.dtype, M, N)
-    with _on(x_q.device):
-        check(lib().aq_int8_mm(px, pxs, pw, pws, py, M, N, K, dt, _stream(x_q.device)), "aq_int8_mm")
+        out = x_q.new_empty((M, N), dtype=dtype)
+    elif not _fits(out, dtype, (M, N), dev):
+        _refuse(x_q, ("out", out, dtype, (M, N)))
+    with _on(dev):
+        st = lib().aq_int8_mm(x_q.data_ptr(), x_scales.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(),
+                              out.data_ptr(), M, N, K, dt, _stream(x_q.device))
+    if st:
+        check(st, "aq_int8_mm")
     return out
 
 
@@ -361,53 +424,74 @@ def aq_qqmm_int8(x, w_q, w_scales, out=None, workspace=None):
     the way and an int8 weight w_q [N, K] with fp32 scales per channel."""
     M, K = _matrix_shape("x", x)
     N = _matrix_shape("w_q", w_q)[0]
-    dt = _dt(x)
+    dt, dev = _dt(x), x.get_device()
+    if not (dev >= 0 and x.is_contiguous() and _fits(w_q, torch.int8, (N, K), dev)
+            and _fits(w_scales, torch.float32, (N,), dev)):
+        _refuse(x, ("x", x, x.dtype, (M, K)), ("w_q", w_q, torch.int8, (N, K)),
+                ("w_scales", w_scales, torch.float32, (N,)))
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
-    _same_device(x, w_q, w_scales, out)
-    px, py = _tensor("x", x, x.dtype, M, K), _tensor("out", out, x.dtype, M, N)
-    pw, pws = _tensor("w_q", w_q, torch.int8, N, K), _tensor("w_scales", w_scales, torch.float32, N)
-    L = lib()
-    with _on(x.device):
-        ws = (workspace or _default_ws).get(
-            x.device, L.aq_workspace_size(AQ_OP_QQMM_INT8, M, N, K, 8, 16, AQ_MODE_AFFINE, 1))
-        check(L.aq_qqmm_int8(px, pw, pws, py, M, N, K, dt, _ptr(ws), 0 if ws is None else ws.numel(),
-                             _stream(x.device)), "aq_qqmm_int8")
+        out = x.new_empty((M, N))
+    elif not _fits(out, x.dtype, (M, N), dev):
+        _refuse(x, ("out", out, x.dtype, (M, N)))
+    need = _qqmm_int8_bytes(M, N, K)
+    with _on(dev):
+        stream = _stream(x.device)
+        ws = _workspace(workspace, x, need, stream, False) if need else None
+        st = lib().aq_qqmm_int8(x.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(), out.data_ptr(), M, N, K,
+                                dt, _ptr(ws), 0 if ws is None else ws.numel(), stream)
+    if st:
+        check(st, "aq_qqmm_int8")
     return out
 
 
-def _moe_matrix(name, m, E, N, K, bits, group_size, dtype, device):
-    """(w_q, scales, biases) of one stack, checked -> the C struct and its mode."""
-    w_q, scales, biases = m
-    _same_device(w_q, scales, biases)
-    if w_q.device != device:
-        raise ValueError("%s is on %s, x on %s" % (name, w_q.device, device))
-    mode = _mode(scales)
-    G = K // group_size if group_size > 0 else 0
-    pw = _tensor(name + " w_q", w_q, torch.uint8, E, N, K * bits // 8)
-    ps = _tensor(name + " scales", scales, torch.uint8 if mode == AQ_MODE_FP4 else dtype, E, N, G)
-    pb = None if biases is None else _tensor(name + " biases", biases, dtype, E, N, G)
-    return _lib.MoeMatrix(pw, ps, pb), mode
+def _moe_stacks(x, H, I, E, gate, up, down, bits, group_size):
+    """Check three stacks (w_q, scales, biases) -> (mode, the C structs' nine
+    addresses).  E and I come from gate."""
+    gs = group_size if group_size > 0 else 1
+    hw, iw = H * bits // 8, I * bits // 8
+    sides = ((gate, (E, I, hw), (E, I, H // gs)), (up, (E, I, hw), (E, I, H // gs)),
+             (down, (E, H, iw), (E, H, I // gs)))
+    dev, mode = x.get_device(), _mode(gate[1])
+    stype = torch.uint8 if mode == AQ_MODE_FP4 else x.dtype
+    at, ok = [], dev >= 0
+    for (w_q, scales, biases), wshape, sshape in sides:
+        ok = ok and _fits(w_q, torch.uint8, wshape, dev) and _fits(scales, stype, sshape, dev)
+        if biases is None:
+            at += (w_q.data_ptr(), scales.data_ptr(), 0)
+        else:
+            ok = ok and _fits(biases, x.dtype, sshape, dev)
+            at += (w_q.data_ptr(), scales.data_ptr(), biases.data_ptr())
+    if not ok:
+        checks = [("x", x, x.dtype, x.shape)]
+        for name, (m, wshape, sshape) in zip(("gate", "up", "down"), sides):
+            if _mode(m[1]) != mode:
+                raise ValueError("gate, up and down must have one format")
+            checks += [(name + " w_q", m[0], torch.uint8, wshape), (name + " scales", m[1], stype, sshape)]
+            if m[2] is not None:
+                checks.append((name + " biases", m[2], x.dtype, sshape))
+        _refuse(x, *checks)
+    return mode, at
 
 
-def _moe_args(x, gate, up, down, bits, group_size, out):
+def _moe_sizes(x, gate):
     T, H = _matrix_shape("x", x)
-    dt = _dt(x)
     if gate[0].dim() != 3:
         raise ValueError("gate w_q must have 3 dimensions, got %d" % gate[0].dim())
-    E, I = gate[0].shape[0], gate[0].shape[1]
-    px = _tensor("x", x, x.dtype, T, H)
-    f = (bits, group_size, x.dtype, x.device)
-    g, mode = _moe_matrix("gate", gate, E, I, H, *f)
-    u, mode_u = _moe_matrix("up", up, E, I, H, *f)
-    d, mode_d = _moe_matrix("down", down, E, H, I, *f)
-    if not mode == mode_u == mode_d:
-        raise ValueError("gate, up and down must have one format")
+    E, I = gate[0].shape[:2]
+    if not x.is_contiguous():
+        _refuse(x, ("x", x, x.dtype, (T, H)))
+    return T, H, I, E
+
+
+def _moe_out(x, out, T, H):
     if out is None:
-        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
-    _same_device(x, out)
-    py = _tensor("out", out, x.dtype, T, H)
-    return T, H, I, E, dt, mode, px, (g, u, d), out, py
+        return torch.empty_like(x)
+    if not _fits(out, x.dtype, (T, H), x.get_device()):
+        _refuse(x, ("out", out, x.dtype, (T, H)))
+    return out
+
+
+_Nine = ctypes.c_uint64 * 9
 
 
 def aq_moe(x, w_router, gate, up, down, top_k, normalize=True, bits=4, group_size=64, out=None,
@@ -416,18 +500,26 @@ def aq_moe(x, w_router, gate, up, down, top_k, normalize=True, bits=4, group_siz
     gate / up (w_q [E, I, H*bits/8], scales and biases [E, I, H/group_size],
     biases None for FP4), down likewise [E, H, I...].  Returns (y [T, H],
     indices int32 [T, top_k], weights fp32 [T, top_k])."""
-    T, H, I, E, dt, mode, px, (g, u, d), out, py = _moe_args(x, gate, up, down, bits, group_size, out)
-    _same_device(x, w_router)
-    pr = _tensor("w_router", w_router, x.dtype, E, H)
+    T, H, I, E = _moe_sizes(x, gate)
+    dt, dev = _dt(x), x.get_device()
+    mode, at = _moe_stacks(x, H, I, E, gate, up, down, bits, group_size)
+    if not _fits(w_router, x.dtype, (E, H), dev):
+        _refuse(x, ("w_router", w_router, x.dtype, (E, H)))
+    out = _moe_out(x, out, T, H)
     k = max(int(top_k), 0)
-    indices = torch.empty((T, k), dtype=torch.int32, device=x.device)
-    weights = torch.empty((T, k), dtype=torch.float32, device=x.device)
-    L = lib()
-    with _on(x.device):
-        ws = (workspace or _default_ws).get(x.device, L.aq_moe_workspace_size(T, H, I, E, k))
-        check(L.aq_moe(px, pr, g, u, d, py, indices.data_ptr(), weights.data_ptr(), T, H, I, E,
-                       top_k, 1 if normalize else 0, bits, group_size, mode, dt, _ptr(ws),
-                       0 if ws is None else ws.numel(), _stream(x.device)), "aq_moe")
+    indices, weights = x.new_empty((T, k), dtype=torch.int32), x.new_empty((T, k), dtype=torch.float32)
+    need = _moe_bytes(T, H, I, E, k)
+    m = _Nine(*at)
+    a = ctypes.addressof(m)
+    with _on(dev):
+        stream = _stream(x.device)
+        ws = _workspace(workspace, x, need, stream, True) if need else None
+        st = _by_address("aq_moe")(x.data_ptr(), w_router.data_ptr(), a, a + 24, a + 48, out.data_ptr(),
+                                   indices.data_ptr(), weights.data_ptr(), T, H, I, E, top_k,
+                                   1 if normalize else 0, bits, group_size, mode, dt, _ptr(ws),
+                                   0 if ws is None else ws.numel(), stream)
+    if st:
+        check(st, "aq_moe")
     return out, indices, weights
 
 
@@ -435,15 +527,32 @@ def aq_moe_experts(x, indices, weights, gate, up, down, bits=4, group_size=64, o
                    workspace=None):
     """The experts of aq_moe for given routing: indices int32 [T, k] and weights
     fp32 [T, k] on the device (an index outside 0..E-1 skips its slot)."""
-    T, H, I, E, dt, mode, px, (g, u, d), out, py = _moe_args(x, gate, up, down, bits, group_size, out)
+    T, H, I, E = _moe_sizes(x, gate)
+    dt, dev = _dt(x), x.get_device()
+    mode, at = _moe_stacks(x, H, I, E, gate, up, down, bits, group_size)
     k = _matrix_shape("indices", indices)[1]
-    _same_device(x, indices, weights)
-    pi = _tensor("indices", indices, torch.int32, T, k)
-    pw = _tensor("weights", weights, torch.float32, T, k)
-    L = lib()
-    with _on(x.device):
-        ws = (workspace or _default_ws).get(x.device, L.aq_moe_workspace_size(T, H, I, E, k))
-        check(L.aq_moe_experts(px, pi, pw, g, u, d, py, T, H, I, E, k, bits, group_size, mode, dt,
-                               _ptr(ws), 0 if ws is None else ws.numel(), _stream(x.device)),
-              "aq_moe_experts")
+    if not (_fits(indices, torch.int32, (T, k), dev) and _fits(weights, torch.float32, (T, k), dev)):
+        _refuse(x, ("indices", indices, torch.int32, (T, k)), ("weights", weights, torch.float32, (T, k)))
+    out = _moe_out(x, out, T, H)
+    need = _moe_bytes(T, H, I, E, k)
+    m = _Nine(*at)
+    a = ctypes.addressof(m)
+    with _on(dev):
+        stream = _stream(x.device)
+        ws = _workspace(workspace, x, need, stream, True) if need else None
+        st = _by_address("aq_moe_experts")(x.data_ptr(), indices.data_ptr(), weights.data_ptr(), a, a + 24,
+                                           a + 48, out.data_ptr(), T, H, I, E, k, bits, group_size, mode, dt,
+                                           _ptr(ws), 0 if ws is None else ws.numel(), stream)
+    if st:
+        check(st, "aq_moe_experts")
     return out
+
+
+@functools.lru_cache(maxsize=None)
+def _by_address(name):
+    """The function with its structs given by address."""
+    f = lib()[name]
+    res, args = _lib.SIGNATURES[name]
+    f.restype = res
+    f.argtypes = [ctypes.c_void_p if a is _lib.MoeMatrixPtr else a for a in args]
+    return f
