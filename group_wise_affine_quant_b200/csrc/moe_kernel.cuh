@@ -181,13 +181,20 @@ __host__ __device__ constexpr float product_scale() {
   return !std::is_same<O, __half>::value ? 1.0f : F::kFp4 ? 16384.0f : 16777216.0f;
 }
 
-template <typename O>
-__device__ __forceinline__ uint32_t e2m1_pair(uint32_t t) {   // codes in bits 0-3 and 16-19
+template <int BY>
+__device__ __forceinline__ uint32_t shifted(uint32_t v) {
+  if constexpr (BY >= 0) return v << BY;
+  else return v >> -BY;
+}
+// The operand word of the E2M1 codes at bits AT and AT + 16 of w.
+template <typename O, int AT>
+__device__ __forceinline__ uint32_t e2m1_pair(uint32_t w) {
+  const uint32_t sign = shifted<12 - AT>(w) & 0x80008000u;
   if constexpr (std::is_same<O, __half>::value) {
-    return ((t & 0x00070007u) << 9) | ((t & 0x00080008u) << 12);
+    return (shifted<9 - AT>(w) & 0x0E000E00u) | sign;
   } else {
     // bits of value * 2^-126 (subnormals are exact), times 2^126
-    const uint32_t v = ((t & 0x00070007u) << 6) | ((t & 0x00080008u) << 12);
+    const uint32_t v = (shifted<6 - AT>(w) & 0x01C001C0u) | sign;
     const uint32_t k = 0x7E807E80u;
     const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
                                      *reinterpret_cast<const __nv_bfloat162*>(&k));
@@ -203,14 +210,20 @@ __device__ __forceinline__ void operand(uint32_t at, int t, uint32_t magic, uint
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const uint32_t w = __byte_perm(g ? lds16<OFF + 8>(at + 2 * t) : lds16<OFF>(at + 2 * t), 0u, 0x4140);
-      r[2 * g] = e2m1_pair<O>(w & 0x000F000Fu);
-      r[2 * g + 1] = e2m1_pair<O>((w >> 4) & 0x000F000Fu);
+      r[2 * g] = e2m1_pair<O, 0>(w);
+      r[2 * g + 1] = e2m1_pair<O, 4>(w);
     }
   } else if constexpr (F::kBits == 4) {
     const uint32_t w = lds32<OFF>(at + 4 * t);
+    if constexpr (F::kFp4) {
+      r[0] = e2m1_pair<O, 0>(w);
+      r[1] = e2m1_pair<O, 4>(w);
+      r[2] = e2m1_pair<O, 8>(w);
+      r[3] = e2m1_pair<O, 12>(w);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r[i] = F::kFp4 ? e2m1_pair<O>((w >> (4 * i)) & 0x000F000Fu) : and_or<0x000F000Fu>(w >> (4 * i), magic);
+      for (int i = 0; i < 4; ++i) r[i] = and_or<0x000F000Fu>(w >> (4 * i), magic);
+    }
   } else if constexpr (F::kBits == 2) {
     const uint32_t w = __byte_perm(lds16<OFF>(at + 2 * t), 0u, 0x4140);
 #pragma unroll
@@ -430,9 +443,15 @@ __device__ __forceinline__ void choose_of(const Params& p, Plan& plan, int warp,
         }
       const unsigned hi = (unsigned)(best >> 32), lo = (unsigned)best;
       const unsigned win_hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-      const unsigned win_lo = __reduce_max_sync(0xFFFFFFFFu, hi == win_hi ? lo : 0u);
-      const bool wins = hi == win_hi && lo == win_lo;
-      const int e = (int)__reduce_min_sync(0xFFFFFFFFu, wins ? (unsigned)(at * 32 + lane) : 0x7FFFFFFFu);
+      const unsigned ahead = __ballot_sync(0xFFFFFFFFu, hi == win_hi);
+      int e;
+      if ((ahead & (ahead - 1)) == 0) {                  // one lane has it
+        e = __shfl_sync(0xFFFFFFFFu, at * 32 + lane, __ffs(ahead) - 1);
+      } else {
+        const unsigned win_lo = __reduce_max_sync(0xFFFFFFFFu, hi == win_hi ? lo : 0u);
+        const bool wins = hi == win_hi && lo == win_lo;
+        e = (int)__reduce_min_sync(0xFFFFFFFFu, wins ? (unsigned)(at * 32 + lane) : 0x7FFFFFFFu);
+      }
       const double l = __shfl_sync(0xFFFFFFFFu, bv, e & 31);
       if (lane == j) {
         mine = e;
@@ -575,16 +594,22 @@ struct Phase {
   int held;                              // chunks of x a warp holds
   int shift, lt, team;                   // log2 of the warps of a team, of the teams
   int pass_chunks, passes;
-  Cursor done, ahead;                    // batch to compute, batch to copy
+  Cursor done;                           // batch to compute
   int turn;                              // batches computed
-  int apass, ai;                         // pass and row tile of the next copy
-  uint32_t at, aat;                      // slots
+  uint32_t at, aat;                      // slots to read, to fill
+  // the next stage to copy: token tile, the team's row tile (of `aend`), pass
+  // and row tile of the batch; addresses and bytes from there on
+  int atile, arb, aend, apass, ai;
+  const uint8_t *pc, *ps;
+  int csize, ssize;
   int tile;                              // whose x is held
   int first, count;                      // its pairs
   // what a thread does the same way in every stage
   int from, n;                           // the warp's chunks of a pass
   const uint8_t *csrc, *ssrc;            // what it copies: codes, scales
   int64_t other;                         // from gate's to up's codes
+  int cstep, sstep;                      // to the team's next row tile
+  bool wide;                             // scales are copied 8 bytes at a time
   uint32_t cdst, sdst;
   uint32_t woff, soff;                   // row g's codes and scales in a slot
   uint32_t own, others;                  // where it puts sums, and gets them to add
@@ -610,7 +635,7 @@ struct Phase {
       : p(pp), plan(pl), ring(ri), warp(w), lane(ln), g(ln >> 2), t(ln & 3),
         K(PH == 1 ? pp.a.H : pp.a.I), chunks(K / 32), blocks(blocks_of(pp)),
         held(PH == 2 && pl.wide ? F::template kHeld<2> : F::template kHeld<1>),
-        lt(teams_of(chunks, held, end - begin)), done(begin, end, blocks, 2 << lt), ahead(done) {
+        lt(teams_of(chunks, held, end - begin)), done(begin, end, blocks, 2 << lt) {
     asm volatile("mov.b32 %0, %1;" : "=r"(magic) : "n"(Op<O>::kMagic));   // not a constant, see and_or
     shift = 4 - lt;
     team = warp >> shift;
@@ -632,8 +657,14 @@ struct Phase {
       const MoeMatrix& m = PH == 2 ? p.a.down : srow < 8 ? p.a.gate : p.a.up;
       ssrc = (arr ? m.biases : m.scales) + (PH == 1 ? srow & 7 : srow) * scale_row;
       sdst = 16 * F::kPitch + (arr * 16 + srow) * F::kScalePitch;
+      cstep = (kRows << lt) * row_bytes;
+      sstep = (kRows << lt) * scale_row;
     }
     settle();
+    atile = done.tile;
+    arb = done.rb + team;
+    aend = min(blocks, end - atile * blocks);
+    open();
     own = exchange + (warp * kExchangeLanes + lane) * 16;
     {
       // 64 pairs of numbers per row tile, each by 4 / teams lanes that add four
@@ -643,11 +674,10 @@ struct Phase {
       jtile = item >> 6;
       jcol = 2 * (src & 3) + (item & 1);
       jrow = src >> 2;
-      others = exchange + (((jtile & 1) * kWarps + ((jtile >> 1) << shift) + part * 4) * kExchangeLanes + src) * 16 +
-               (item & 1) * 8;
+      const int first_warp = (jtile >> lt) * kWarps + ((jtile & ((1 << lt) - 1)) << shift) + part * 4;
+      others = exchange + (first_warp * kExchangeLanes + src) * 16 + (item & 1) * 8;
       if (part) jtile |= 64;             // adds, but does not store
     }
-    skip();
   }
 
   // The warp's chunks of a pass: whole groups.
@@ -675,55 +705,78 @@ struct Phase {
   __device__ __forceinline__ int row0(int tl, int rb) const {
     return plan.tile_expert[tl] * (PH == 1 ? p.a.I : p.a.H) + rb * kRows;
   }
-  // The team's row tiles of a batch: up to 2.
-  __device__ __forceinline__ int mine(const Cursor& c) const { return min(2, c.nb - 2 * team); }
-  __device__ __forceinline__ void skip() {
-    while (ahead.more() && mine(ahead) <= 0) ahead.next();
+  // Row tile j of a batch is team j % teams'; a team has up to 2.
+  __device__ __forceinline__ int mine(const Cursor& c) const {
+    return min(2, (c.nb - team + (1 << lt) - 1) >> lt);
   }
 
-  // Start the copies of the warp's next stage: its part of a row tile.  Rows
-  // need not be aligned: the copy takes the aligned window around a part (a
-  // stack ends on a multiple of 16 bytes).
+  // Move on to a token tile where the team has a row tile, if there is one.
+  __device__ __forceinline__ void open() {
+    while (arb >= aend && (atile + 1) * blocks < done.end) {
+      ++atile;
+      arb = team;
+      aend = min(blocks, done.end - atile * blocks);
+    }
+    if (arb < aend) aim();
+  }
+  // Addresses of the stage: a row need not be aligned, the copy takes the
+  // aligned window around the warp's part (a stack ends on a multiple of 16
+  // bytes).
+  __device__ __forceinline__ void aim() {
+    int f = from, m = n;
+    if (passes > 1) place(apass, f, m);
+    const int row = row0(atile, arb + (ai << lt));
+    const int off = code_at(apass, f), skew = ((lane >> 3) * row_bytes + off) & 15;
+    pc = csrc + ((int64_t)row * row_bytes + (off - skew));
+    csize = m > 0 ? skew + m * 4 * F::kBits - (lane & 7) * 16 : 0;
+    ps = ssrc + ((int64_t)row * scale_row + scale_at(apass, f));
+    ssize = F::kFp4 && lane >= 16 ? 0 : m * 32 / F::kGs * F::kScaleSize;
+    wide = F::kScaleBytes % 8 == 0 && (scale_row | scale_at(apass, f)) % 8 == 0;
+    if (!wide) {
+      const int sk = (int)(reinterpret_cast<uintptr_t>(ps) & 3);
+      ps -= sk;
+      if (ssize) ssize += sk;
+    }
+  }
+
+  // Start the copies of the warp's next stage: its part of a row tile.
   __device__ __forceinline__ void issue() {
-    if (ahead.more()) {
-      int f = from, m = n;
-      if (passes > 1) place(apass, f, m);
-      const int row = row0(ahead.tile, ahead.rb + 2 * team + ai);
-      {
-        const int off = code_at(apass, f), skew = ((lane >> 3) * row_bytes + off) & 15;
-        const uint8_t* src = csrc + ((int64_t)row * row_bytes + (off - skew));
+    if (arb < aend) {
+      if (csize > 0) {
         const uint32_t dst = aat + cdst;
-        if ((lane & 7) * 16 < skew + m * 4 * F::kBits && m > 0) {
-          cp_async<16>(dst, src);
-          cp_async<16>(dst + 4 * F::kPitch, src + 4 * row_bytes);
-          cp_async<16>(dst + 8 * F::kPitch, src + other);
-          cp_async<16>(dst + 12 * F::kPitch, src + other + 4 * row_bytes);
-        }
+        const uint8_t* far = pc + other;
+        cp_async<16>(dst, pc);
+        cp_async<16>(dst + 4 * F::kPitch, pc + 4 * row_bytes);
+        cp_async<16>(dst + 8 * F::kPitch, far);
+        cp_async<16>(dst + 12 * F::kPitch, far + 4 * row_bytes);
       }
-      if (m > 0 && (!F::kFp4 || lane < 16)) {
-        const int off = scale_at(apass, f), bytes = m * 32 / F::kGs * F::kScaleSize;
-        const uint8_t* src = ssrc + ((int64_t)row * scale_row + off);
-        const uint32_t dst = aat + sdst;
-        if (F::kScaleBytes % 8 == 0 && (scale_row | off) % 8 == 0) {
+      const uint32_t dst = aat + sdst;
+      if (wide) {
 #pragma unroll
-          for (int u = 0; u < F::kScaleBytes; u += 8)
-            if (u < bytes) cp_async<8>(dst + u, src + u);
-        } else {
-          const int skew = (int)(reinterpret_cast<uintptr_t>(src) & 3);
+        for (int u = 0; u < F::kScaleBytes; u += 8)
+          if (u < ssize) cp_async<8>(dst + u, ps + u);
+      } else {
 #pragma unroll
-          for (int u = 0; u < 4 * F::kScaleWords; u += 4)
-            if (u < skew + bytes) cp_async<4>(dst + u, src - skew + u);
-        }
-      }
-      if (++ai == mine(ahead)) {
-        ai = 0;
-        if (++apass == passes) {
-          apass = 0;
-          ahead.next();
-          skip();
-        }
+        for (int u = 0; u < 4 * F::kScaleWords; u += 4)
+          if (u < ssize) cp_async<4>(dst + u, ps + u);
       }
       aat = next(aat);
+      if (passes == 1) {
+        arb += 1 << lt;
+        pc += cstep;
+        ps += sstep;
+        if (arb >= aend) open();
+      } else {
+        if (++ai == 2 || arb + (ai << lt) >= aend) {
+          ai = 0;
+          if (++apass == passes) {
+            apass = 0;
+            arb += 2 << lt;
+          }
+        }
+        if (arb >= aend) open();
+        else aim();
+      }
     }
     cp_commit();
   }
@@ -796,7 +849,16 @@ struct Phase {
     uint32_t b;
     if constexpr (F::kFp4) {
       asm volatile("ld.shared.u8 %0, [%1+%2];" : "=r"(b) : "r"(at), "n"(OFF));
-      return fp4_scale_t<T>(b, F::kGs);
+      if constexpr (F::kGs == 16) {
+        // E4M3 values are exact in both T
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)b));
+        return __half2float(__ushort_as_half((unsigned short)h));
+      } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        return e8m0_to_float(b);                         // exact in bf16
+      } else {
+        return fp4_scale_t<T>(b, F::kGs);
+      }
     } else {
       asm volatile("ld.shared.u16 %0, [%1+%2];" : "=r"(b) : "r"(at), "n"(OFF));
       if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(b << 16);
