@@ -339,12 +339,15 @@ constexpr int kExchangeBytes = 2 * 2 * kWarps * kExchangeLanes * 16;
 constexpr int kRingAt = (kExchangeAt + kExchangeBytes + 127) / 128 * 128;
 constexpr int kRingBytes = (227 * 1024 - kRingAt) / kWarps / 16 * 16;   // a warp's
 
-// Every CTA of the (cooperative, so co-resident) grid arrives; false after the
-// time limit.
-__device__ __forceinline__ bool grid_barrier(unsigned* counter, unsigned ctas, int* abort) {
+// The CTA arrives at a barrier of the (cooperative, so co-resident) grid, with
+// all its writes so far; what does not need the others goes before the wait.
+__device__ __forceinline__ void grid_arrive(unsigned* counter) {
   __syncthreads();
+  if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
+}
+// Until every CTA has arrived; false after the time limit.
+__device__ __forceinline__ bool grid_wait(unsigned* counter, unsigned ctas, int* abort) {
   if (threadIdx.x == 0) {
-    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
     const uint64_t t0 = globaltimer_ns();
     for (unsigned it = 1;; ++it) {
       unsigned v;
@@ -604,6 +607,7 @@ struct Phase {
   int csize, ssize;
   int tile;                              // whose x is held
   int first, count;                      // its pairs
+  bool fresh;                            // it is still on its way
   // what a thread does the same way in every stage
   int from, n;                           // the warp's chunks of a pass
   const uint8_t *csrc, *ssrc;            // what it copies: codes, scales
@@ -646,6 +650,7 @@ struct Phase {
     apass = ai = turn = 0;
     at = aat = ring;
     tile = -1;
+    fresh = false;
     place(0, from, n);
     {
       // codes: eight lanes to a row, four rows at a time; scales and biases: a
@@ -796,7 +801,7 @@ struct Phase {
   float sum[kParts][2];
 
   template <int NB>
-  __device__ __forceinline__ void load(int chunk, int n) {
+  __device__ __forceinline__ void load(int chunk) {
     const uint8_t* col = nullptr;
     const int at = PH == 2 && NB == 1 ? g & 3 : g;
     if (at < count) {
@@ -823,6 +828,10 @@ struct Phase {
         xv[c * NB + b] = v;
       }
     }
+  }
+  // What there is to do with it once it has come.
+  template <int NB>
+  __device__ __forceinline__ void prepare() {
 #pragma unroll
     for (int k = 0; k < F::template kHeld<NB> / kGu; ++k) {
       float S[4] = {0.f, 0.f, 0.f, 0.f};
@@ -964,6 +973,21 @@ struct Phase {
     }
   }
 
+  // Ask for the batch's x: it comes while the warp waits for its copies.
+  __device__ __forceinline__ void fetch(int pass) {
+    if (!done.more()) return;
+    tile = done.tile;
+    first = plan.tile_first[tile];
+    count = plan.tile_count[tile];
+    if (passes > 1) {
+      place(pass, from, n);
+      settle(pass);
+    }
+    if (PH == 2 && count > 4) load<PH>(pass * pass_chunks + from);
+    else load<1>(pass * pass_chunks + from);
+    fresh = true;
+  }
+
   // A warp waits for its own copies only, and all meet once per batch: the
   // barrier publishes the batch's sums, and the buffer of the batch after next
   // is written by warps past the next barrier.
@@ -971,22 +995,17 @@ struct Phase {
     while (done.more()) {
       const int nb = mine(done);
       for (int pass = 0; pass < passes; ++pass) {
-        if (done.tile != tile || passes > 1) {
-          tile = done.tile;
-          first = plan.tile_first[tile];
-          count = plan.tile_count[tile];
-          if (passes > 1) {
-            place(pass, from, n);
-            settle(pass);
-          }
-          if (PH == 2 && count > 4) load<PH>(pass * pass_chunks + from, n);
-          else load<1>(pass * pass_chunks + from, n);
-        }
+        if (done.tile != tile || passes > 1) fetch(pass);
         uint32_t to = own + (turn & 1) * kBuffer;
         for (int i = 0; i < nb; ++i) {
           cp_wait<kSlots - 2>();
           __syncwarp();
           issue();
+          if (fresh) {
+            fresh = false;
+            if (PH == 2 && count > 4) prepare<PH>();
+            else prepare<1>();
+          }
           float tot[4] = {0.f, 0.f, 0.f, 0.f};
           if (PH == 2 && count > 4) products<PH>(tot);
           else products<1>(tot);
@@ -1027,7 +1046,7 @@ __device__ __forceinline__ void weighted_sums(const Params& p, const Plan& plan)
        q += (int)gridDim.x * kThreads) {
     const int tok = q / vecs, v = q - tok * vecs;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
     for (int j = 0; j < k; ++j) {
       const int pair = tok * k + j;
       if (plan.expert[pair] >= 0) {
@@ -1059,7 +1078,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   bool ok = true;
   if (p.a.w_router) {
     router_logits<T>(p, warp, lane);
-    ok = grid_barrier(p.bars + 0, gridDim.x, &plan.abort);
+    grid_arrive(p.bars + 0);
+    ok = grid_wait(p.bars + 0, gridDim.x, &plan.abort);
     if (ok) choose(p, plan, warp, lane);
   } else {
     for (int q = threadIdx.x; q < p.a.T * p.a.top_k; q += kThreads) {
@@ -1076,16 +1096,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       using Up = Phase<1, T, F>;
       Up up(p, plan, ring, exchange, warp, lane, Up::border(p, plan, blockIdx.x),
             Up::border(p, plan, blockIdx.x + 1));
+      up.fetch(0);
       up.start();
       up.run();
     }
+    grid_arrive(p.bars + 1);             // h is written
     Down down(p, plan, ring, exchange, warp, lane, Down::border(p, plan, blockIdx.x),
               Down::border(p, plan, blockIdx.x + 1));
     down.start();
-    ok = grid_barrier(p.bars + 1, gridDim.x, &plan.abort);
+    ok = grid_wait(p.bars + 1, gridDim.x, &plan.abort);
     if (ok) {
       down.run();
-      ok = grid_barrier(p.bars + 2, gridDim.x, &plan.abort);
+      grid_arrive(p.bars + 2);
+      ok = grid_wait(p.bars + 2, gridDim.x, &plan.abort);
       if (ok) weighted_sums<T>(p, plan);
     }
   }
