@@ -48,6 +48,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxPairs = 1024;          // tokens * top_k
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTopK = 16;
+constexpr int kBatch = 4;                // row tiles of a team between two barriers (even)
 constexpr int kExchangeLanes = 33;       // a lane more, to spread the banks
 constexpr int kCounterBytes = 65536;     // the workspace's shared counter area
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -323,19 +324,18 @@ struct Plan {
   int16_t rank[kMaxPairs];               // of a pair among its expert's
   int16_t order[kMaxPairs];              // pairs by expert
   int16_t tile_expert[kMaxPairs];
-  int16_t tile_first[kMaxPairs];         // into order
-  uint8_t tile_count[kMaxPairs];
+  int16_t tile_first[kMaxPairs + 1];     // into order; the next tile's is its end
   int16_t count[kMaxExperts];
   int16_t first[kMaxExperts];
   int scan[2][kWarps];
   int tiles;
-  int wide;                              // some tile has more than four pairs
+  int wide;                              // tiles have up to 8 pairs, else up to 4
   int abort;
 };
 
 // Shared memory: plan, the sums that warps exchange, the ring.
 constexpr int kExchangeAt = (int)((sizeof(Plan) + 15) / 16 * 16);
-constexpr int kExchangeBytes = 2 * 2 * kWarps * kExchangeLanes * 16;
+constexpr int kExchangeBytes = 2 * kBatch * kWarps * kExchangeLanes * 16;
 constexpr int kRingAt = (kExchangeAt + kExchangeBytes + 127) / 128 * 128;
 constexpr int kRingBytes = (227 * 1024 - kRingAt) / kWarps / 16 * 16;   // a warp's
 
@@ -510,8 +510,10 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan& plan) {
     }
   }
   __syncthreads();
-  const int c = tid < E ? plan.count[tid] : 0, n = (c + 7) / 8;
-  int sc = c, sn = n;
+  // Tiles of up to 8 pairs, or of 4 if that makes few more (their h fits one
+  // operand, as hi and lo columns): scanned side by side.
+  const int c = tid < E ? plan.count[tid] : 0, both = (c + 7) / 8 | (c + 3) / 4 << 16;
+  int sc = c, sn = both;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int uc = __shfl_up_sync(0xFFFFFFFFu, sc, o), un = __shfl_up_sync(0xFFFFFFFFu, sn, o);
@@ -525,21 +527,29 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan& plan) {
     plan.scan[1][warp] = sn;
   }
   __syncthreads();
-  int bc = 0, bn = 0;
-  for (int w = 0; w < warp; ++w) {
-    bc += plan.scan[0][w];
-    bn += plan.scan[1][w];
+  int bc = 0, bn = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int ac = plan.scan[0][w], an = plan.scan[1][w];
+    total += an;
+    if (w < warp) {
+      bc += ac;
+      bn += an;
+    }
   }
-  const int c0 = bc + sc - c, n0 = bn + sn - n;
+  const bool wide = (total >> 16) * 8 > (total & 0xFFFF) * 9;
+  const int cap = wide ? 8 : 4, shift = wide ? 0 : 16;
+  const int c0 = bc + sc - c, n0 = ((bn + sn - both) >> shift) & 0xFFFF, n = (both >> shift) & 0xFFFF;
   if (tid < E) plan.first[tid] = c0;
   for (int j = 0; j < n; ++j) {
     plan.tile_expert[n0 + j] = (int16_t)tid;
-    plan.tile_first[n0 + j] = (int16_t)(c0 + 8 * j);
-    plan.tile_count[n0 + j] = (uint8_t)min(8, c - 8 * j);
+    plan.tile_first[n0 + j] = (int16_t)(c0 + cap * j);
   }
-  if (tid == kThreads - 1) plan.tiles = bn + sn;
-  const int wide = __syncthreads_or(c > 4);
-  if (tid == 0) plan.wide = wide;
+  if (tid == kThreads - 1) {
+    plan.tiles = (total >> shift) & 0xFFFF;
+    plan.tile_first[plan.tiles] = (int16_t)(bc + sc);
+    plan.wide = wide;
+  }
   __syncthreads();
   for (int q = tid; q < P; q += kThreads) {
     const int e = plan.expert[q];
@@ -586,7 +596,7 @@ struct Phase {
   static constexpr int kRows = PH == 1 ? 8 : 16;         // rows of a matrix in a row tile
   static constexpr int kSlots = kRingBytes / F::kSlot < 6 ? kRingBytes / F::kSlot : 6;
   static_assert(kSlots >= 3, "ring");
-  static constexpr uint32_t kBuffer = 2 * kWarps * kExchangeLanes * 16;
+  static constexpr uint32_t kBuffer = kBatch * kWarps * kExchangeLanes * 16;
 
   const Params& p;
   const Plan& plan;
@@ -639,7 +649,7 @@ struct Phase {
       : p(pp), plan(pl), ring(ri), warp(w), lane(ln), g(ln >> 2), t(ln & 3),
         K(PH == 1 ? pp.a.H : pp.a.I), chunks(K / 32), blocks(blocks_of(pp)),
         held(PH == 2 && pl.wide ? F::template kHeld<2> : F::template kHeld<1>),
-        lt(teams_of(chunks, held, end - begin)), done(begin, end, blocks, 2 << lt) {
+        lt(teams_of(chunks, held, end - begin)), done(begin, end, blocks, kBatch << lt) {
     asm volatile("mov.b32 %0, %1;" : "=r"(magic) : "n"(Op<O>::kMagic));   // not a constant, see and_or
     shift = 4 - lt;
     team = warp >> shift;
@@ -712,7 +722,7 @@ struct Phase {
   }
   // Row tile j of a batch is team j % teams'; a team has up to 2.
   __device__ __forceinline__ int mine(const Cursor& c) const {
-    return min(2, (c.nb - team + (1 << lt) - 1) >> lt);
+    return min(kBatch, (c.nb - team + (1 << lt) - 1) >> lt);
   }
 
   // Move on to a token tile where the team has a row tile, if there is one.
@@ -772,11 +782,11 @@ struct Phase {
         ps += sstep;
         if (arb >= aend) open();
       } else {
-        if (++ai == 2 || arb + (ai << lt) >= aend) {
+        if (++ai == kBatch || arb + (ai << lt) >= aend) {
           ai = 0;
           if (++apass == passes) {
             apass = 0;
-            arb += 2 << lt;
+            arb += kBatch << lt;
           }
         }
         if (arb >= aend) open();
@@ -919,40 +929,44 @@ struct Phase {
   }
   template <int NB>
   __device__ __forceinline__ void products(float (&tot)[4]) {
-    constexpr int kFull = F::template kHeld<NB>, kHalf = kFull / 2;
+    constexpr int kFull = F::template kHeld<NB>, kMost = kFull * 3 / 4;
     const uint32_t w = at + woff, s = at + soff;
     float P[4];
     if (n == kFull) multiply<NB, kFull>(tot, P, w, s);
-    else if (kHalf % kGu == 0 && n == kHalf) multiply<NB, kHalf % kGu == 0 ? kHalf : kFull>(tot, P, w, s);
+    else if (kMost % kGu == 0 && n == kMost) multiply<NB, kMost % kGu == 0 ? kMost : kFull>(tot, P, w, s);
     else multiply<NB, 0>(tot, P, w, s);
   }
 
   // The sums of a batch over the warps of each team.
   __device__ __forceinline__ void join() {
-    const bool live = (jtile & 63) < done.nb;
-    float a = 0.0f, b = 0.0f;
-    if (live) {
-      const uint32_t o = others + (turn & 1) * kBuffer;
+#pragma unroll 1
+    for (int i = 0; i < kBatch && i << lt < done.nb; i += 2) {
+      const int jt = jtile + (i << lt);
+      const bool live = (jt & 63) < done.nb;
+      float a = 0.0f, b = 0.0f;
+      if (live) {
+        const uint32_t o = others + (turn & 1) * kBuffer + i * (kWarps * kExchangeLanes * 16);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float2 v = lds_f2(o + m * (kExchangeLanes * 16));
-        a += v.x;
-        b += v.y;
+        for (int m = 0; m < 4; ++m) {
+          const float2 v = lds_f2(o + m * (kExchangeLanes * 16));
+          a += v.x;
+          b += v.y;
+        }
       }
-    }
-    if (lt < 2) {
-      a += __shfl_xor_sync(0xFFFFFFFFu, a, 1);
-      b += __shfl_xor_sync(0xFFFFFFFFu, b, 1);
-      if (lt < 1) {
-        a += __shfl_xor_sync(0xFFFFFFFFu, a, 2);
-        b += __shfl_xor_sync(0xFFFFFFFFu, b, 2);
+      if (lt < 2) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, 1);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, 1);
+        if (lt < 1) {
+          a += __shfl_xor_sync(0xFFFFFFFFu, a, 2);
+          b += __shfl_xor_sync(0xFFFFFFFFu, b, 2);
+        }
       }
+      if (PH == 2 && count <= 4) {                       // columns of hi and lo
+        a += __shfl_down_sync(0xFFFFFFFFu, a, 16 >> lt);
+        b += __shfl_down_sync(0xFFFFFFFFu, b, 16 >> lt);
+      }
+      if (jt < done.nb && jcol < count) store(a, b, plan.order[first + jcol], done.rb + jt, jrow);
     }
-    if (PH == 2 && count <= 4) {                         // columns of hi and lo
-      a += __shfl_down_sync(0xFFFFFFFFu, a, 16 >> lt);
-      b += __shfl_down_sync(0xFFFFFFFFu, b, 16 >> lt);
-    }
-    if (jtile < done.nb && jcol < count) store(a, b, plan.order[first + jcol], done.rb + jtile, jrow);
   }
 
   // A pair of sums: (gate, up) of one h, or rows g and g + 8 of down's result.
@@ -978,7 +992,7 @@ struct Phase {
     if (!done.more()) return;
     tile = done.tile;
     first = plan.tile_first[tile];
-    count = plan.tile_count[tile];
+    count = plan.tile_first[tile + 1] - first;
     if (passes > 1) {
       place(pass, from, n);
       settle(pass);
