@@ -447,30 +447,39 @@ def aq_qqmm_int8(x, w_q, w_scales, out=None, workspace=None):
 def _moe_stacks(x, H, I, E, gate, up, down, bits, group_size):
     """Check three stacks (w_q, scales, biases) -> (mode, the C structs' nine
     addresses).  E and I come from gate."""
-    gs = group_size if group_size > 0 else 1
-    hw, iw = H * bits // 8, I * bits // 8
-    sides = ((gate, (E, I, hw), (E, I, H // gs)), (up, (E, I, hw), (E, I, H // gs)),
-             (down, (E, H, iw), (E, H, I // gs)))
-    dev, mode = x.get_device(), _mode(gate[1])
-    stype = torch.uint8 if mode == AQ_MODE_FP4 else x.dtype
-    at, ok = [], dev >= 0
-    for (w_q, scales, biases), wshape, sshape in sides:
-        ok = ok and _fits(w_q, torch.uint8, wshape, dev) and _fits(scales, stype, sshape, dev)
-        if biases is None:
-            at += (w_q.data_ptr(), scales.data_ptr(), 0)
-        else:
-            ok = ok and _fits(biases, x.dtype, sshape, dev)
-            at += (w_q.data_ptr(), scales.data_ptr(), biases.data_ptr())
-    if not ok:
-        checks = [("x", x, x.dtype, x.shape)]
-        for name, (m, wshape, sshape) in zip(("gate", "up", "down"), sides):
-            if _mode(m[1]) != mode:
-                raise ValueError("gate, up and down must have one format")
-            checks += [(name + " w_q", m[0], torch.uint8, wshape), (name + " scales", m[1], stype, sshape)]
-            if m[2] is not None:
-                checks.append((name + " biases", m[2], x.dtype, sshape))
-        _refuse(x, *checks)
-    return mode, at
+    (gq, gs, gb), (uq, us, ub), (dq, ds, db) = gate, up, down
+    unit = group_size if group_size > 0 else 1
+    wide, deep = (E, I, H * bits // 8), (E, H, I * bits // 8)        # codes
+    wscale, dscale = (E, I, H // unit), (E, H, I // unit)
+    dtype, dev, u8 = x.dtype, x.get_device(), torch.uint8
+    mode = AQ_MODE_FP4 if gs.dtype is u8 else AQ_MODE_AFFINE
+    stype = u8 if mode else dtype
+    if (dev >= 0 and _fits(gq, u8, wide, dev) and _fits(uq, u8, wide, dev) and _fits(dq, u8, deep, dev)
+            and _fits(gs, stype, wscale, dev) and _fits(us, stype, wscale, dev)
+            and _fits(ds, stype, dscale, dev)):
+        if gb is None and ub is None and db is None:
+            return mode, (gq.data_ptr(), gs.data_ptr(), 0, uq.data_ptr(), us.data_ptr(), 0,
+                          dq.data_ptr(), ds.data_ptr(), 0)
+        if (gb is not None and ub is not None and db is not None and _fits(gb, dtype, wscale, dev)
+                and _fits(ub, dtype, wscale, dev) and _fits(db, dtype, dscale, dev)):
+            return mode, (gq.data_ptr(), gs.data_ptr(), gb.data_ptr(), uq.data_ptr(), us.data_ptr(),
+                          ub.data_ptr(), dq.data_ptr(), ds.data_ptr(), db.data_ptr())
+    checks = [("x", x, dtype, x.shape)]
+    for name, (w_q, scales, biases), w, s in (("gate", gate, wide, wscale), ("up", up, wide, wscale),
+                                              ("down", down, deep, dscale)):
+        if _mode(scales) != mode or (biases is None) != (gb is None):
+            raise ValueError("gate, up and down must have one format")
+        checks += [(name + " w_q", w_q, u8, w), (name + " scales", scales, stype, s)]
+        if biases is not None:
+            checks.append((name + " biases", biases, dtype, s))
+    _refuse(x, *checks)
+
+
+# Allocating a tensor like another takes 1.4 us, by shape and type 2.1.
+@functools.lru_cache(maxsize=256)
+def _routing(T, k, dev):
+    return (torch.empty((T, k), dtype=torch.int32, device=dev),
+            torch.empty((T, k), dtype=torch.float32, device=dev))
 
 
 def _moe_sizes(x, gate):
@@ -507,7 +516,8 @@ def aq_moe(x, w_router, gate, up, down, top_k, normalize=True, bits=4, group_siz
         _refuse(x, ("w_router", w_router, x.dtype, (E, H)))
     out = _moe_out(x, out, T, H)
     k = max(int(top_k), 0)
-    indices, weights = x.new_empty((T, k), dtype=torch.int32), x.new_empty((T, k), dtype=torch.float32)
+    indices, weights = _routing(T, k, dev)
+    indices, weights = torch.empty_like(indices), torch.empty_like(weights)
     need = _moe_bytes(T, H, I, E, k)
     m = _Nine(*at)
     a = ctypes.addressof(m)
