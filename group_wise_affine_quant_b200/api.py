@@ -8,7 +8,6 @@ affine scales / biases are T [N, K/group_size]; FP4 scales are uint8.  The
 W8A8 functions take int8 codes and fp32 scales; the mixture-of-experts ones
 take stacks [E, ...] of the same weights.
 """
-import contextlib
 import ctypes
 import functools
 
@@ -328,33 +327,42 @@ def _matrix_shape(name, t):
     return t.shape
 
 
-_no_guard = contextlib.nullcontext()
-
-
-def _on(dev):
-    """Make device number `dev` the current one for a launch."""
-    return _no_guard if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+def _launch(x, fn, what, *args):
+    """Call `fn` on x's device and its current stream (the last argument)."""
+    dev = x.get_device()
+    if dev == torch.cuda.current_device():
+        st = fn(*args, _stream(x.device))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(x.device))
+    if st:
+        check(st, what)
 
 
 _scratch = {}
 
 
-def _workspace(workspace, x, nbytes, stream, counters):
-    """The caller's Workspace, or a buffer of this device and stream (calls on
-    two streams may overlap); a call that is being captured gets one of its
-    own, which lives in the graph's memory."""
+def _workspace(workspace, x, nbytes, counters):
+    """(address, bytes) of the caller's Workspace, or of a buffer of this device
+    and stream (calls on two streams may overlap); a call that is being captured
+    gets one of its own, which lives in the graph's memory."""
+    if nbytes == 0:
+        return None, 0
     if workspace is not None:
-        return workspace.get(x.device, nbytes)
-    if torch.cuda.is_current_stream_capturing():
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        if counters:
-            buf[:_COUNTER_BYTES].zero_()
-        return buf
-    key = (x.get_device(), stream)
-    buf = _scratch.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = _scratch[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=x.device)
-    return buf
+        buf = workspace.get(x.device, nbytes)
+    elif torch.cuda.is_current_stream_capturing():
+        with torch.cuda.device(x.device):
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+            if counters:
+                buf[:_COUNTER_BYTES].zero_()
+    else:
+        key = (x.get_device(), _stream(x.device))
+        buf = _scratch.get(key)
+        if buf is None or buf.numel() < nbytes:
+            with torch.cuda.device(x.device):
+                buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=x.device)
+            _scratch[key] = buf
+    return buf.data_ptr(), buf.numel()
 
 
 _COUNTER_BYTES = 65536           # at a workspace's start, zero between calls (include/aq.h)
@@ -384,10 +392,7 @@ def aq_quantize_int8(x, out=None):
         q, s = out
         if not (_fits(q, torch.int8, shape, dev) and _fits(s, torch.float32, (R,), dev)):
             _refuse(x, ("codes", q, torch.int8, shape), ("scales", s, torch.float32, (R,)))
-    with _on(dev):
-        st = lib().aq_quantize_int8(x.data_ptr(), q.data_ptr(), s.data_ptr(), R, K, dt, _stream(x.device))
-    if st:
-        check(st, "aq_quantize_int8")
+    _launch(x, lib().aq_quantize_int8, "aq_quantize_int8", x.data_ptr(), q.data_ptr(), s.data_ptr(), R, K, dt)
     return q, s
 
 
@@ -411,11 +416,8 @@ def aq_int8_mm(x_q, x_scales, w_q, w_scales, dtype=torch.bfloat16, out=None):
         out = x_q.new_empty((M, N), dtype=dtype)
     elif not _fits(out, dtype, (M, N), dev):
         _refuse(x_q, ("out", out, dtype, (M, N)))
-    with _on(dev):
-        st = lib().aq_int8_mm(x_q.data_ptr(), x_scales.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(),
-                              out.data_ptr(), M, N, K, dt, _stream(x_q.device))
-    if st:
-        check(st, "aq_int8_mm")
+    _launch(x_q, lib().aq_int8_mm, "aq_int8_mm", x_q.data_ptr(), x_scales.data_ptr(), w_q.data_ptr(),
+            w_scales.data_ptr(), out.data_ptr(), M, N, K, dt)
     return out
 
 
@@ -433,14 +435,9 @@ def aq_qqmm_int8(x, w_q, w_scales, out=None, workspace=None):
         out = x.new_empty((M, N))
     elif not _fits(out, x.dtype, (M, N), dev):
         _refuse(x, ("out", out, x.dtype, (M, N)))
-    need = _qqmm_int8_bytes(M, N, K)
-    with _on(dev):
-        stream = _stream(x.device)
-        ws = _workspace(workspace, x, need, stream, False) if need else None
-        st = lib().aq_qqmm_int8(x.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(), out.data_ptr(), M, N, K,
-                                dt, _ptr(ws), 0 if ws is None else ws.numel(), stream)
-    if st:
-        check(st, "aq_qqmm_int8")
+    ws, nbytes = _workspace(workspace, x, _qqmm_int8_bytes(M, N, K), False)
+    _launch(x, lib().aq_qqmm_int8, "aq_qqmm_int8", x.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(),
+            out.data_ptr(), M, N, K, dt, ws, nbytes)
     return out
 
 
@@ -518,18 +515,12 @@ def aq_moe(x, w_router, gate, up, down, top_k, normalize=True, bits=4, group_siz
     k = max(int(top_k), 0)
     indices, weights = _routing(T, k, dev)
     indices, weights = torch.empty_like(indices), torch.empty_like(weights)
-    need = _moe_bytes(T, H, I, E, k)
+    ws, nbytes = _workspace(workspace, x, _moe_bytes(T, H, I, E, k), True)
     m = _Nine(*at)
     a = ctypes.addressof(m)
-    with _on(dev):
-        stream = _stream(x.device)
-        ws = _workspace(workspace, x, need, stream, True) if need else None
-        st = _by_address("aq_moe")(x.data_ptr(), w_router.data_ptr(), a, a + 24, a + 48, out.data_ptr(),
-                                   indices.data_ptr(), weights.data_ptr(), T, H, I, E, top_k,
-                                   1 if normalize else 0, bits, group_size, mode, dt, _ptr(ws),
-                                   0 if ws is None else ws.numel(), stream)
-    if st:
-        check(st, "aq_moe")
+    _launch(x, _by_address("aq_moe"), "aq_moe", x.data_ptr(), w_router.data_ptr(), a, a + 24, a + 48,
+            out.data_ptr(), indices.data_ptr(), weights.data_ptr(), T, H, I, E, top_k,
+            1 if normalize else 0, bits, group_size, mode, dt, ws, nbytes)
     return out, indices, weights
 
 
@@ -544,17 +535,12 @@ def aq_moe_experts(x, indices, weights, gate, up, down, bits=4, group_size=64, o
     if not (_fits(indices, torch.int32, (T, k), dev) and _fits(weights, torch.float32, (T, k), dev)):
         _refuse(x, ("indices", indices, torch.int32, (T, k)), ("weights", weights, torch.float32, (T, k)))
     out = _moe_out(x, out, T, H)
-    need = _moe_bytes(T, H, I, E, k)
+    ws, nbytes = _workspace(workspace, x, _moe_bytes(T, H, I, E, k), True)
     m = _Nine(*at)
     a = ctypes.addressof(m)
-    with _on(dev):
-        stream = _stream(x.device)
-        ws = _workspace(workspace, x, need, stream, True) if need else None
-        st = _by_address("aq_moe_experts")(x.data_ptr(), indices.data_ptr(), weights.data_ptr(), a, a + 24,
-                                           a + 48, out.data_ptr(), T, H, I, E, k, bits, group_size, mode, dt,
-                                           _ptr(ws), 0 if ws is None else ws.numel(), stream)
-    if st:
-        check(st, "aq_moe_experts")
+    _launch(x, _by_address("aq_moe_experts"), "aq_moe_experts", x.data_ptr(), indices.data_ptr(),
+            weights.data_ptr(), a, a + 24, a + 48, out.data_ptr(), T, H, I, E, k, bits, group_size, mode, dt,
+            ws, nbytes)
     return out
 
 
