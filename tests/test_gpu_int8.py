@@ -213,6 +213,43 @@ def test_chain_on_a_stream_and_in_a_graph():
     assert api.lib().aq_device_errors() == 0
 
 
+def test_weights_written_just_before():
+    """The product of aq_qqmm_int8 reads its weights early, yet after a kernel
+    that writes them on the same stream."""
+    K, N = 4096, 2048
+    x = to_dev(normal((4, K), 1.0, 1, gen(3)))
+    a = api.aq_quantize_int8(to_dev(normal((N, K), 0.02, 1, gen(4))))
+    b = api.aq_quantize_int8(to_dev(normal((N, K), 0.02, 1, gen(5))))
+    xq, xs = api.aq_quantize_int8(x)
+    wq, ws = torch.empty_like(a[0]), torch.empty_like(a[1])
+    got = []
+    for i in range(20):
+        src = (a, b)[i % 2]
+        wq.copy_(src[0])
+        ws.copy_(src[1])
+        got.append(api.aq_qqmm_int8(x, wq, ws))
+    for i, y in enumerate(got):
+        src = (a, b)[i % 2]
+        assert torch.equal(y, mm_ref(xq, xs, *src, y.dtype))
+
+
+def test_two_streams_with_the_default_scratch():
+    K = 1024
+    wq, ws = api.aq_quantize_int8(to_dev(normal((512, K), 0.02, 1, gen(6))))
+    x = [to_dev(normal((64, K), 1.0, 1, gen(s))) for s in (7, 8)]
+    want = [mm_ref(*api.aq_quantize_int8(v), wq, ws, v.dtype) for v in x]
+    streams = [torch.cuda.Stream() for _ in x]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for j in range(2):
+            with torch.cuda.stream(streams[j]):
+                got[j].append(api.aq_qqmm_int8(x[j], wq, ws))
+    torch.cuda.synchronize()
+    for j in range(2):
+        assert all(torch.equal(y, want[j]) for y in got[j])
+
+
 def test_weight_prefetch_setting():
     """With the thread's weight prefetch on, after a kernel that writes x only."""
     wq, ws = api.aq_quantize_int8(to_dev(normal((4096, 2048), 0.02, 1, gen(1))))

@@ -1,7 +1,8 @@
 """GPU tests of the mixture-of-experts layer (aq_moe, aq_moe_experts) against
 its formula in 64 bits: every weight format, group size and type, one token to
 64, odd group counts per row, slots without an expert, an expert named twice,
-ties and NaN among the logits, captured replays, streams and workspaces."""
+ties and NaN among the logits, captured replays, streams and workspaces, and
+the layer among W8A8 projections."""
 import numpy as np
 import pytest
 import torch
@@ -108,6 +109,43 @@ def test_widths(H, I, dt):
     L = Layer(4, H, I, gs=32, dt=dt, seed=H + I)
     x = L.x(3)
     L.check_moe(x, 2, False, api.aq_moe(x, L.router, *L.m, 2, False, **L.kw))
+    errors()
+
+
+@pytest.mark.parametrize("fmt,bits,gs,H,I", [
+    ("affine", 4, 64, 8256, 64),        # gate and up rows in three pieces, the last a single group
+    ("affine", 4, 32, 64, 4128),        # down
+    ("affine", 8, 64, 4160, 2112),      # both, 8-bit rows
+    ("affine", 3, 64, 4160, 2112),      # rows that start at any 4 bytes
+    ("affine", 6, 32, 2080, 2080),
+    ("affine", 2, 128, 8320, 128),
+    ("fp4", 4, 32, 4128, 2080),         # scale rows of odd length
+    ("fp4", 4, 16, 8224, 4128)])
+@pytest.mark.parametrize("T", [2, 7])
+def test_rows_in_several_passes(fmt, bits, gs, H, I, T):
+    """Rows longer than a CTA's warps hold at once, with token tiles of up to 4
+    (T = 2) and of up to 8 pairs (T = 7, all at one expert)."""
+    L = Layer(2, H, I, fmt, bits, gs, 1, seed=bits + T)
+    x = L.x(T)
+    indices = torch.zeros((T, 1), dtype=torch.int32, device=DEV)
+    if T == 2:
+        indices[1] = 1
+    weights = torch.full((T, 1), 0.25, device=DEV)
+    y = api.aq_moe_experts(x, indices, weights, *L.m, **L.kw)
+    L.check_experts(x, indices, weights, y)
+    errors()
+
+
+@pytest.mark.parametrize("counts", [[4, 4, 4], [5, 1, 1], [8, 1, 0], [9, 9, 0], [12, 3, 1], [20, 2, 2], [33, 0, 1]])
+def test_pairs_per_expert(counts):
+    """Token tiles of 4 and of 8 pairs, full and cut off."""
+    L = Layer(len(counts), 192, 96, gs=32, seed=sum(counts))
+    order = [e for e, c in enumerate(counts) for _ in range(c)]
+    T = len(order)
+    indices = torch.tensor(order, dtype=torch.int32)[torch.randperm(T, generator=gen(T))].view(T, 1).to(DEV)
+    weights = torch.rand((T, 1), device=DEV)
+    x = L.x(T)
+    L.check_experts(x, indices, weights, api.aq_moe_experts(x, indices, weights, *L.m, **L.kw))
     errors()
 
 
@@ -259,6 +297,80 @@ def test_two_streams_at_once():
     for j in range(2):
         for o in got[j]:
             assert all(torch.equal(a, b) for a, b in zip(o, want[j]))
+
+
+def test_two_streams_with_the_default_scratch():
+    L = Layer(8, 512, 256, seed=19)
+    xs = [L.x(3, s) for s in (51, 52)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    want = [api.aq_moe(x, L.router, *L.m, 2, True, **L.kw) for x in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for j in range(2):
+            with torch.cuda.stream(streams[j]):
+                got[j].append(api.aq_moe(xs[j], L.router, *L.m, 2, True, **L.kw))
+    errors()
+    for j in range(2):
+        for o in got[j]:
+            assert all(torch.equal(a, b) for a, b in zip(o, want[j]))
+
+
+def test_two_graphs_with_the_default_scratch():
+    """Each captured call has scratch of its own: replays on two streams at once
+    and eager calls beside them."""
+    L = Layer(8, 512, 256, seed=20)
+    xs = [L.x(3, s) for s in (61, 62)]
+    want = [api.aq_moe(x, L.router, *L.m, 2, True, **L.kw) for x in xs]
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in xs], []
+    for g, x in zip(graphs, xs):
+        with torch.cuda.graph(g):
+            outs.append(api.aq_moe(x, L.router, *L.m, 2, True, **L.kw))
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(10):
+        for j in range(2):
+            with torch.cuda.stream(streams[j]):
+                graphs[j].replay()
+        eager = api.aq_moe(xs[0], L.router, *L.m, 2, True, **L.kw)
+    errors()
+    for j in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(outs[j], want[j]))
+    assert all(torch.equal(a, b) for a, b in zip(eager, want[0]))
+
+
+def test_linear_layers_of_a_block():
+    """The operators together, as a decoder block's linear layers use them: an
+    8-bit projection, the mixture of experts, a second projection, two tokens
+    in decode and then five; eagerly, and captured once per count."""
+    H, E = 256, 6
+    L = Layer(E, H, 128, seed=21)
+    proj = [api.aq_quantize_int8(to_dev(normal((H, H), 0.06, 1, gen(s)))) for s in (71, 72)]
+
+    def block(x):
+        a = api.aq_qqmm_int8(x, *proj[0])
+        y, indices, weights = api.aq_moe(a, L.router, *L.m, 2, True, **L.kw)
+        return a, y, indices, weights, api.aq_qqmm_int8(y, *proj[1])
+
+    def check(x, out):
+        a, y, indices, weights, z = out
+        L.check_moe(a, 2, True, (y, indices, weights))
+        for src, (wq, ws), got in ((x, proj[0], a), (y, proj[1], z)):
+            xq, xs = api.aq_quantize_int8(src)
+            exact = (xq.double() @ wq.double().T).float()
+            assert torch.equal(got, ((exact * xs[:, None]) * ws[None, :]).to(got.dtype))
+    for T in (2, 5):
+        x = L.x(T)
+        check(x, block(x))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = block(x)
+        for seed in (81, 82):
+            x.copy_(L.x(T, seed))
+            g.replay()
+            torch.cuda.synchronize()
+            check(x, out)
+    errors()
 
 
 def test_refuses_what_the_kernel_cannot_take():
