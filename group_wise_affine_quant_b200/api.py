@@ -39,13 +39,15 @@ def _ptr(t):
 
 # torch.cuda.current_stream builds an object for each call (2.3 us of a call's
 # 10); the handle alone takes 0.1.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(device):
-    if _raw_stream is None or device.index is None:
+    if device.index is None:
         return torch.cuda.current_stream(device).cuda_stream
-    return _raw_stream(device.index)
+    return _stream_of(device.index)
 
 
 def _mode(scales):
@@ -327,18 +329,6 @@ def _matrix_shape(name, t):
     return t.shape
 
 
-def _launch(x, fn, what, *args):
-    """Call `fn` on x's device and its current stream (the last argument)."""
-    dev = x.get_device()
-    if dev == torch.cuda.current_device():
-        st = fn(*args, _stream(x.device))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream(x.device))
-    if st:
-        check(st, what)
-
-
 _scratch = {}
 
 
@@ -351,17 +341,15 @@ def _workspace(workspace, x, nbytes, counters):
     if workspace is not None:
         buf = workspace.get(x.device, nbytes)
     elif torch.cuda.is_current_stream_capturing():
-        with torch.cuda.device(x.device):
-            buf = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-            if counters:
-                buf[:_COUNTER_BYTES].zero_()
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        if counters:
+            buf[:_COUNTER_BYTES].zero_()
     else:
-        key = (x.get_device(), _stream(x.device))
+        dev = x.get_device()
+        key = (dev, _stream_of(dev))
         buf = _scratch.get(key)
         if buf is None or buf.numel() < nbytes:
-            with torch.cuda.device(x.device):
-                buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=x.device)
-            _scratch[key] = buf
+            buf = _scratch[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=x.device)
     return buf.data_ptr(), buf.numel()
 
 
@@ -378,21 +366,30 @@ def _moe_bytes(T, H, I, E, k):
     return lib().aq_moe_workspace_size(T, H, I, E, k)
 
 
+# The functions below launch on the current device: they call themselves with it
+# changed where x is on another.  (torch.empty is faster with the sizes as
+# arguments than with a tuple or as a method.)
+
+
 def aq_quantize_int8(x, out=None):
     """x [R, K] fp16/bf16 -> (codes int8 [R, K], scales fp32 [R]): a symmetric
     scale per row (a token, or a channel of a weight)."""
-    shape = _matrix_shape("x", x)
+    R, K = _matrix_shape("x", x)
     dt, dev = _dt(x), x.get_device()
-    R, K = shape
     if dev < 0 or not x.is_contiguous():
-        _refuse(x, ("x", x, x.dtype, shape))
+        _refuse(x, ("x", x, x.dtype, x.shape))
     if out is None:
-        q, s = torch.empty_like(x, dtype=torch.int8), x.new_empty((R,), dtype=torch.float32)
+        q, s = torch.empty_like(x, dtype=torch.int8), torch.empty(R, dtype=torch.float32, device=x.device)
     else:
         q, s = out
-        if not (_fits(q, torch.int8, shape, dev) and _fits(s, torch.float32, (R,), dev)):
-            _refuse(x, ("codes", q, torch.int8, shape), ("scales", s, torch.float32, (R,)))
-    _launch(x, lib().aq_quantize_int8, "aq_quantize_int8", x.data_ptr(), q.data_ptr(), s.data_ptr(), R, K, dt)
+        if not (_fits(q, torch.int8, (R, K), dev) and _fits(s, torch.float32, (R,), dev)):
+            _refuse(x, ("codes", q, torch.int8, (R, K)), ("scales", s, torch.float32, (R,)))
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return aq_quantize_int8(x, (q, s))
+    st = lib().aq_quantize_int8(x.data_ptr(), q.data_ptr(), s.data_ptr(), R, K, dt, _stream_of(dev))
+    if st:
+        check(st, "aq_quantize_int8")
     return q, s
 
 
@@ -413,11 +410,16 @@ def aq_int8_mm(x_q, x_scales, w_q, w_scales, dtype=torch.bfloat16, out=None):
         _refuse(x_q, ("x_q", x_q, i8, (M, K)), ("x_scales", x_scales, f32, (M,)),
                 ("w_q", w_q, i8, (N, K)), ("w_scales", w_scales, f32, (N,)))
     if out is None:
-        out = x_q.new_empty((M, N), dtype=dtype)
+        out = torch.empty(M, N, dtype=dtype, device=x_q.device)
     elif not _fits(out, dtype, (M, N), dev):
         _refuse(x_q, ("out", out, dtype, (M, N)))
-    _launch(x_q, lib().aq_int8_mm, "aq_int8_mm", x_q.data_ptr(), x_scales.data_ptr(), w_q.data_ptr(),
-            w_scales.data_ptr(), out.data_ptr(), M, N, K, dt)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return aq_int8_mm(x_q, x_scales, w_q, w_scales, dtype, out)
+    st = lib().aq_int8_mm(x_q.data_ptr(), x_scales.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(),
+                          out.data_ptr(), M, N, K, dt, _stream_of(dev))
+    if st:
+        check(st, "aq_int8_mm")
     return out
 
 
@@ -432,12 +434,17 @@ def aq_qqmm_int8(x, w_q, w_scales, out=None, workspace=None):
         _refuse(x, ("x", x, x.dtype, (M, K)), ("w_q", w_q, torch.int8, (N, K)),
                 ("w_scales", w_scales, torch.float32, (N,)))
     if out is None:
-        out = x.new_empty((M, N))
+        out = torch.empty(M, N, dtype=x.dtype, device=x.device)
     elif not _fits(out, x.dtype, (M, N), dev):
         _refuse(x, ("out", out, x.dtype, (M, N)))
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return aq_qqmm_int8(x, w_q, w_scales, out, workspace)
     ws, nbytes = _workspace(workspace, x, _qqmm_int8_bytes(M, N, K), False)
-    _launch(x, lib().aq_qqmm_int8, "aq_qqmm_int8", x.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(),
-            out.data_ptr(), M, N, K, dt, ws, nbytes)
+    st = lib().aq_qqmm_int8(x.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(), out.data_ptr(), M, N, K, dt,
+                            ws, nbytes, _stream_of(dev))
+    if st:
+        check(st, "aq_qqmm_int8")
     return out
 
 
@@ -470,13 +477,6 @@ def _moe_stacks(x, H, I, E, gate, up, down, bits, group_size):
         if biases is not None:
             checks.append((name + " biases", biases, dtype, s))
     _refuse(x, *checks)
-
-
-# Allocating a tensor like another takes 1.4 us, by shape and type 2.1.
-@functools.lru_cache(maxsize=256)
-def _routing(T, k, dev):
-    return (torch.empty((T, k), dtype=torch.int32, device=dev),
-            torch.empty((T, k), dtype=torch.float32, device=dev))
 
 
 def _moe_sizes(x, gate):
@@ -512,15 +512,20 @@ def aq_moe(x, w_router, gate, up, down, top_k, normalize=True, bits=4, group_siz
     if not _fits(w_router, x.dtype, (E, H), dev):
         _refuse(x, ("w_router", w_router, x.dtype, (E, H)))
     out = _moe_out(x, out, T, H)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return aq_moe(x, w_router, gate, up, down, top_k, normalize, bits, group_size, out, workspace)
     k = max(int(top_k), 0)
-    indices, weights = _routing(T, k, dev)
-    indices, weights = torch.empty_like(indices), torch.empty_like(weights)
+    indices = torch.empty(T, k, dtype=torch.int32, device=x.device)
+    weights = torch.empty(T, k, dtype=torch.float32, device=x.device)
     ws, nbytes = _workspace(workspace, x, _moe_bytes(T, H, I, E, k), True)
     m = _Nine(*at)
     a = ctypes.addressof(m)
-    _launch(x, _by_address("aq_moe"), "aq_moe", x.data_ptr(), w_router.data_ptr(), a, a + 24, a + 48,
-            out.data_ptr(), indices.data_ptr(), weights.data_ptr(), T, H, I, E, top_k,
-            1 if normalize else 0, bits, group_size, mode, dt, ws, nbytes)
+    st = _by_address("aq_moe")(x.data_ptr(), w_router.data_ptr(), a, a + 24, a + 48, out.data_ptr(),
+                               indices.data_ptr(), weights.data_ptr(), T, H, I, E, top_k,
+                               1 if normalize else 0, bits, group_size, mode, dt, ws, nbytes, _stream_of(dev))
+    if st:
+        check(st, "aq_moe")
     return out, indices, weights
 
 
@@ -535,12 +540,17 @@ def aq_moe_experts(x, indices, weights, gate, up, down, bits=4, group_size=64, o
     if not (_fits(indices, torch.int32, (T, k), dev) and _fits(weights, torch.float32, (T, k), dev)):
         _refuse(x, ("indices", indices, torch.int32, (T, k)), ("weights", weights, torch.float32, (T, k)))
     out = _moe_out(x, out, T, H)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return aq_moe_experts(x, indices, weights, gate, up, down, bits, group_size, out, workspace)
     ws, nbytes = _workspace(workspace, x, _moe_bytes(T, H, I, E, k), True)
     m = _Nine(*at)
     a = ctypes.addressof(m)
-    _launch(x, _by_address("aq_moe_experts"), "aq_moe_experts", x.data_ptr(), indices.data_ptr(),
-            weights.data_ptr(), a, a + 24, a + 48, out.data_ptr(), T, H, I, E, k, bits, group_size, mode, dt,
-            ws, nbytes)
+    st = _by_address("aq_moe_experts")(x.data_ptr(), indices.data_ptr(), weights.data_ptr(), a, a + 24, a + 48,
+                                       out.data_ptr(), T, H, I, E, k, bits, group_size, mode, dt, ws, nbytes,
+                                       _stream_of(dev))
+    if st:
+        check(st, "aq_moe_experts")
     return out
 
 
