@@ -364,9 +364,8 @@ __device__ __forceinline__ bool grid_wait(unsigned* counter, unsigned ctas, int*
         break;
       }
     }
-    __threadfence();
   }
-  __syncthreads();
+  __syncthreads();                       // the acquire holds for the whole CTA
   return *(volatile int*)abort == 0;
 }
 
@@ -565,6 +564,13 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan& plan) {
 }
 
 // ------------------------------------------------------- gate/up and down
+// a / b for 0 <= a < 2^24, b > 0: rounded division, put right by at most one.
+__device__ __forceinline__ int quotient(int a, int b) {
+  int q = (int)__fdividef((float)a, (float)b);
+  const int r = a - q * b;
+  return r < 0 ? q - 1 : r >= b ? q + 1 : q;
+}
+
 // The row tiles of one phase in a CTA, [m, end), in batches: up to `most`
 // neighbouring row tiles of one token tile.
 struct Cursor {
@@ -572,7 +578,7 @@ struct Cursor {
   int tile, rb, nb;                      // token tile, first row tile, row tiles
   __device__ __forceinline__ Cursor(int begin, int e, int bl, int mo)
       : m(begin), end(e), blocks(bl), most(mo) {
-    tile = begin / bl;
+    tile = quotient(begin, bl);
     rb = begin - tile * bl;
     size();
   }
@@ -638,9 +644,10 @@ struct Phase {
   static __device__ __forceinline__ int blocks_of(const Params& p) {
     return PH == 1 ? p.a.I / 8 : p.a.H / 16;
   }
-  // At most 1024 token tiles of 8192 row tiles each: the product fits 32 bits.
-  static __device__ __forceinline__ int border(const Params& p, const Plan& plan, int cta) {
-    return (int)((unsigned)(plan.tiles * blocks_of(p)) * (unsigned)cta / gridDim.x);
+  // Where the share of the CTA with this fraction (of 2^32) of the grid before
+  // it begins.
+  static __device__ __forceinline__ int border(const Params& p, const Plan& plan, unsigned share) {
+    return (int)__umulhi((unsigned)(plan.tiles * blocks_of(p)), share);
   }
   // log2 of the teams: as few warps to a team as hold K, but no more teams than
   // pairs of row tiles.
@@ -662,7 +669,8 @@ struct Phase {
     row_bytes = chunks * 4 * F::kBits;
     scale_row = K / F::kGs * F::kScaleSize;
     pass_chunks = held << shift;
-    passes = (chunks + pass_chunks - 1) / pass_chunks;
+    const int log = shift + (held == 8 ? 3 : 2);
+    passes = (chunks + pass_chunks - 1) >> log;
     apass = ai = turn = 0;
     at = aat = ring;
     tile = -1;
@@ -1095,6 +1103,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   const uint32_t ring = smem_u32(smem) + kRingAt + warp * kRingBytes;
   if (threadIdx.x == 0) plan.abort = 0;
 
+  // The grid's row tiles are cut at these fractions of 2^32 (the last CTA ends
+  // with the last tile).
+  const unsigned step = 0xFFFFFFFFu / gridDim.x;
+  const unsigned share = step * blockIdx.x;
+  const bool last = blockIdx.x == gridDim.x - 1;
+
   bool ok = true;
   if (p.a.w_router) {
     router_logits<T>(p, warp, lane);
@@ -1114,15 +1128,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     using Down = Phase<2, T, F>;
     {
       using Up = Phase<1, T, F>;
-      Up up(p, plan, ring, exchange, warp, lane, Up::border(p, plan, blockIdx.x),
-            Up::border(p, plan, blockIdx.x + 1));
+      Up up(p, plan, ring, exchange, warp, lane, Up::border(p, plan, share),
+            last ? plan.tiles * Up::blocks_of(p) : Up::border(p, plan, share + step));
       up.fetch(0);
       up.start();
       up.run();
     }
     grid_arrive(p.bars + 1);             // h is written
-    Down down(p, plan, ring, exchange, warp, lane, Down::border(p, plan, blockIdx.x),
-              Down::border(p, plan, blockIdx.x + 1));
+    Down down(p, plan, ring, exchange, warp, lane, Down::border(p, plan, share),
+              last ? plan.tiles * Down::blocks_of(p) : Down::border(p, plan, share + step));
     down.start();
     ok = grid_wait(p.bars + 1, gridDim.x, &plan.abort);
     if (ok) {
