@@ -951,12 +951,13 @@ struct Phase {
     else multiply<NB, 0>(tot, P, w, s);
   }
 
-  // The sums of a batch over the warps of each team.
-  __device__ __forceinline__ void join() {
+  // The sums of a batch (its first row tile and how many, its pairs) over the
+  // warps of each team.
+  __device__ __forceinline__ void join(int rb, int nb, int first, int count) {
 #pragma unroll 1
-    for (int i = 0; i < kBatch && i << lt < done.nb; i += 2) {
+    for (int i = 0; i < kBatch && i << lt < nb; i += 2) {
       const int jt = jtile + (i << lt);
-      const bool live = (jt & 63) < done.nb;
+      const bool live = (jt & 63) < nb;
       float a = 0.0f, b = 0.0f;
       if (live) {
         const uint32_t o = others + (turn & 1) * kBuffer + i * (kWarps * kExchangeLanes * 16);
@@ -979,7 +980,7 @@ struct Phase {
         a += __shfl_down_sync(0xFFFFFFFFu, a, 16 >> lt);
         b += __shfl_down_sync(0xFFFFFFFFu, b, 16 >> lt);
       }
-      if (jt < done.nb && jcol < count) store(a, b, plan.order[first + jcol], done.rb + jt, jrow);
+      if (jt < nb && jcol < count) store(a, b, plan.order[first + jcol], rb + jt, jrow);
     }
   }
 
@@ -1056,10 +1057,12 @@ struct Phase {
           to += kWarps * kExchangeLanes * 16;
         }
       }
-      __syncthreads();
-      join();
-      ++turn;
+      const int rb = done.rb, nt = done.nb, of = first, pairs = count;
       done.next();
+      if (done.tile != tile && passes == 1) fetch(0);    // the next x comes meanwhile
+      __syncthreads();
+      join(rb, nt, of, pairs);
+      ++turn;
     }
   }
 };
