@@ -580,14 +580,54 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
             }
           } else {
             __syncwarp();
-            const int rows = min(32, a.M - row0);
-            for (int r = 0; r < rows; ++r) {
+            const int rows = min(32, a.M - row0), cols = min(64, a.N - n0);
+            T* to = y + (int64_t)row0 * a.N + n0;
+            // (eight reads before their stores, which the compiler takes for
+            // ones that might change what is read)
+            if (a.N % 4 == 0) {
+              // rows start at a multiple of 8 bytes: two at a time
+              const int c = lane & 15;
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int c = 32 * i + lane;
-                if (n0 + c < a.N)
-                  y[(int64_t)(row0 + r) * a.N + n0 + c] = *reinterpret_cast<const T*>(
-                      out + r * 128 + (((c >> 3) ^ (r & 7)) * 16) + (c & 7) * 2);
+              for (int i = 0; i < 16; i += 8) {
+                uint2 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int r = 2 * (i + k) + (lane >> 4);
+                  v[k] = *reinterpret_cast<const uint2*>(out + r * 128 + (((c >> 1) ^ (r & 7)) * 16) + (c & 1) * 8);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int r = 2 * (i + k) + (lane >> 4);
+                  if (r < rows && 4 * c < cols) *reinterpret_cast<uint2*>(to + (int64_t)r * a.N + 4 * c) = v[k];
+                }
+              }
+            } else {
+              // pairs from the row's first multiple of 4 bytes on, and what is
+              // left at its ends
+              auto at = [&](int r, int c) {
+                return *reinterpret_cast<const uint16_t*>(out + r * 128 + (((c >> 3) ^ (r & 7)) * 16) + (c & 7) * 2);
+              };
+              uint16_t* row = reinterpret_cast<uint16_t*>(to);
+#pragma unroll 1
+              for (int r = 0; r < rows; r += 8) {
+                uint32_t v[8], first[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int odd = (int)(((row0 + k) & a.N) & 1);       // n0 and r are even
+                  const int c = 2 * lane + odd;
+                  v[k] = at(r + k, c) | (uint32_t)at(r + k, (c + 1) & 63) << 16;
+                  first[k] = at(r + k, 0);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int odd = (int)(((row0 + k) & a.N) & 1), c = 2 * lane + odd;
+                  if (r + k < rows) {
+                    if (c + 1 < cols) *reinterpret_cast<uint32_t*>(row + c) = v[k];
+                    else if (c < cols) row[c] = (uint16_t)v[k];
+                    if (odd && lane == 0 && cols > 0) row[0] = (uint16_t)first[k];
+                  }
+                  row += a.N;
+                }
               }
             }
           }
