@@ -269,6 +269,16 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t a, uint64_t b, 
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// Two values rounded to T, a in the low half.
+template <typename T> __device__ __forceinline__ uint32_t pack_t(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack_t<__half>(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack_t<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 // Arrive on the barrier at this offset in both CTAs of the pair once the MMAs
 // issued so far have completed.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
@@ -513,17 +523,34 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
     T* y = static_cast<T*>(a.y);
     uint32_t tile_i = 0;
     bool ok = true;
+    // The scales of a tile's columns and of the thread's row are asked for a
+    // tile ahead.
+    float column = 0.0f, row = 0.0f;
+    auto ask = [&](int t) {
+      if (t >= tiles) return;
+      int mt, nt;
+      tile_at(t, a.m_tiles, a.n_tiles, mt, nt);
+      if constexpr (PAIR) {
+        const int m = mt * kRowsA + (int)rank * kBM + q * 32 + lane;
+        column = et < BN && nt * BN + et < a.N ? a.ws[nt * BN + et] : 0.0f;
+        row = m < a.M ? a.xs[m] : 0.0f;
+      } else {
+        const int n = nt * kBM + q * 32 + lane;
+        column = et < BN && mt * BN + et < a.M ? a.xs[mt * BN + et] : 0.0f;
+        row = n < a.N ? a.ws[n] : 0.0f;
+      }
+    };
+    static_assert(BN <= kEt, "a column to a thread");
+    ask(first);
     for (int t = first; t < tiles; t += step, ++tile_i) {
       int mt, nt;
       tile_at(t, a.m_tiles, a.n_tiles, mt, nt);
       const int b = (int)(tile_i & 1u);
       float* sxb = sx + b * BN;                          // scales of the columns
-      if constexpr (PAIR) {
-        for (int i = et; i < BN; i += kEt) sxb[i] = nt * BN + i < a.N ? a.ws[nt * BN + i] : 0.0f;
-      } else {
-        for (int i = et; i < BN; i += kEt) sxb[i] = mt * BN + i < a.M ? a.xs[mt * BN + i] : 0.0f;
-      }
+      if (et < BN) sxb[et] = column;
+      const float s_row = row;
       named_barrier_sync(1, kEt);
+      ask(t + step);
       // after giving up the warps still meet at the barrier above
       if (ok) ok = mbar_wait(tfull(b), (tile_i >> 1) & 1u, abort_flag);
       if (!ok) continue;
@@ -531,13 +558,10 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN);
       if constexpr (PAIR) {
         const int row0 = mt * kRowsA + (int)rank * kBM + q * 32;   // the warp's tokens
-        const float sm = row0 + lane < a.M ? a.xs[row0 + lane] : 0.0f;
         uint8_t* out = smem_raw + (base - raw) + ST * S::kStage + (warp - 2) * 4096;
         const int end = (warp - 2) / 4 * (BN / 2) + BN / 2;
 #pragma unroll 1
         for (int c0 = end - BN / 2; c0 < end; c0 += 64) {
-          if (lane == 0) bulk_wait_read<0>();            // the last store has left
-          __syncwarp();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t r[32];
@@ -546,24 +570,24 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
 #pragma unroll
             for (int i = 0; i < 8; ++i) sc[i] = *reinterpret_cast<const float4*>(sxb + c0 + 32 * h + 4 * i);
             tmem_ld_wait();
-            auto v = [&](int c, float w) {
-              return TT<T>::from_f(__fmul_rn(__fmul_rn(__int2float_rn((int)r[c]), sm), w));
-            };
+            auto v = [&](int c, float w) { return __fmul_rn(__fmul_rn(__int2float_rn((int)r[c]), s_row), w); };
+            uint4 o[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              T o[8];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float4 w = sc[2 * u + i];
-                o[4 * i] = v(8 * u + 4 * i, w.x);
-                o[4 * i + 1] = v(8 * u + 4 * i + 1, w.y);
-                o[4 * i + 2] = v(8 * u + 4 * i + 2, w.z);
-                o[4 * i + 3] = v(8 * u + 4 * i + 3, w.w);
-              }
-              // 128-byte rows, 16-byte units swizzled by the row
-              *reinterpret_cast<uint4*>(out + lane * 128 + (((4 * h + u) ^ (lane & 7)) * 16)) =
-                  *reinterpret_cast<const uint4*>(o);
+              const float4 a0 = sc[2 * u], a1 = sc[2 * u + 1];
+              o[u] = make_uint4(pack_t<T>(v(8 * u, a0.x), v(8 * u + 1, a0.y)),
+                                pack_t<T>(v(8 * u + 2, a0.z), v(8 * u + 3, a0.w)),
+                                pack_t<T>(v(8 * u + 4, a1.x), v(8 * u + 5, a1.y)),
+                                pack_t<T>(v(8 * u + 6, a1.z), v(8 * u + 7, a1.w)));
             }
+            if (h == 0) {
+              if (lane == 0) bulk_wait_read<0>();        // the last store has left
+              __syncwarp();
+            }
+            // 128-byte rows, 16-byte units swizzled by the row
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              *reinterpret_cast<uint4*>(out + lane * 128 + (((4 * h + u) ^ (lane & 7)) * 16)) = o[u];
           }
           if (c0 + 64 >= end) {                          // the accumulator is free
             tc_fence_before();
@@ -635,7 +659,6 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
       } else {
         const int m0 = mt * BN;
         const int n = nt * kBM + q * 32 + lane;
-        const float sw = n < a.N ? a.ws[n] : 0.0f;
         constexpr int kCols = BN < 32 ? BN : 32;
 #pragma unroll 1
         for (int c0 = 0; c0 < BN; c0 += kCols) {
@@ -657,7 +680,7 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
                 const float4 v = sc[c / 4];
                 const float s = c % 4 == 0 ? v.x : c % 4 == 1 ? v.y : c % 4 == 2 ? v.z : v.w;
                 if (c < cols)
-                  out[(int64_t)c * a.N] = TT<T>::from_f(__fmul_rn(__fmul_rn(__int2float_rn((int)r[c]), s), sw));
+                  out[(int64_t)c * a.N] = TT<T>::from_f(__fmul_rn(__fmul_rn(__int2float_rn((int)r[c]), s), s_row));
               }
             }
           } else {
@@ -848,9 +871,10 @@ Int8Plan plan_int8_mm(int64_t M, int64_t N, int64_t K) {
     bool pair;
     int block, full, start, column;      // clocks: per block, more at full load, start, per column
   };
-  static const Tile kTiles[6] = {{16, false, 458, 135, 4366, 90},  {32, false, 462, 160, 4800, 90},
-                                 {64, false, 469, 55, 6200, 90},   {128, false, 502, 134, 8700, 90},
-                                 {128, true, 389, 65, 6750, 14},   {256, true, 500, 130, 8500, 14}};
+  static const Tile kTiles[6] = {{16, false, 458, 135, 4366, 130}, {32, false, 462, 160, 4800, 130},
+                                 {64, false, 469, 55, 6200, 75},   {128, false, 502, 134, 8700, 75},
+                                 {128, true, 389, 65, 6750, 23},   {256, true, 500, 130, 8500, 20}};
+  const int ragged = N % 8 == 0 ? 0 : N % 4 == 0 ? 9 : 29;           // rows of y that TMA cannot store
   static const int kSlotsTwo[9] = {0, 296, 148, 93, 71, 56, 45, 37, 33};   // two CTAs on an SM
   static const int kSlotsOne[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
   Int8Plan best{};
@@ -871,7 +895,7 @@ Int8Plan plan_int8_mm(int64_t M, int64_t N, int64_t K) {
       if ((kblocks + kb - 1) / kb != s) continue;        // an empty slice
       const double waves = (double)((tiles + slots - 1) / slots);
       const double load = tiles < slots ? (double)tiles / slots : 1.0;
-      const double products = kb * (t.block + t.full * load), stores = t.column * columns * load;
+      const double products = kb * (t.block + t.full * load), stores = (t.column + (t.pair ? ragged : 0)) * columns * load;
       const double cost = waves * (products > stores ? products : stores) +
                           (s > 1 ? 5400.0 + 10.0 * t.bn + 30.0 * columns + 150.0 * s
                                  : t.start + (t.pair ? 0.0 : 25.0 * columns));
