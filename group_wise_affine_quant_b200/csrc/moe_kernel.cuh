@@ -77,10 +77,9 @@ struct Format {
   static constexpr int kGs = GS;
   static constexpr bool kFp4 = FP4;
   // Which of a thread's 8 codes of a 32-chunk form its operand words: halves
-  // (j, j + 4) where masks take both at once, neighbours where codes are cut
-  // out one by one; for groups of 16 a thread holds 4 codes of each group.
-  static constexpr Order kOrder = GS == 16 ? Order::kGroup16
-                                  : (BITS == 2 || BITS == 4) ? Order::kSplit : Order::kPairs;
+  // (j, j + 4) where masks take both at once, neighbours for whole bytes; for
+  // groups of 16 a thread holds 4 codes of each group.
+  static constexpr Order kOrder = GS == 16 ? Order::kGroup16 : BITS == 8 ? Order::kPairs : Order::kSplit;
   static constexpr int kScaleSize = FP4 ? 1 : 2;
   // 32-chunks of x a warp holds with NB operands each: what the registers take,
   // and what lets two stages of 16 warps' chunks fit the ring.
@@ -258,17 +257,21 @@ __device__ __forceinline__ void operand(uint32_t at, int t, uint32_t magic, uint
     const uint32_t byte = F::kBits * t;
     const uint32_t w0 = lds32<OFF>(at + (byte & ~3u)), w1 = lds32<OFF + 4>(at + (byte & ~3u));
     const uint32_t sh = (byte & 3u) * 8u;
-    const uint32_t v[2] = {__funnelshift_r(w0, w1, sh), w1 >> sh};
-    constexpr uint32_t mask = (1u << F::kBits) - 1u;
+    const uint32_t v = __funnelshift_r(w0, w1, sh);
+    if constexpr (F::kBits == 3) {
+      // codes 0-3 to the low half, 4-7 to the high one
+      const uint32_t w = (v & 0x00000FFFu) | ((v << 4) & 0x0FFF0000u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t q[2];
+      for (int i = 0; i < 4; ++i) r[i] = and_or<0x00070007u>(w >> (3 * i), magic);
+    } else {
+      // codes 4-7 in a word of their own, then as many as fit 16 bits and the rest
+      constexpr int kHalf = 4 * F::kBits, kFit = F::kBits == 5 ? 3 : 2, kSkip = kFit * F::kBits;
+      constexpr uint32_t mask = F::kBits == 5 ? 0x001F001Fu : 0x003F003Fu;
+      const uint32_t u = __funnelshift_r(v, w1 >> sh, kHalf);
+      const uint32_t a = __byte_perm(v, u, 0x5410), b = __byte_perm(v >> kSkip, u >> kSkip, 0x5410);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int bit = F::kBits * (2 * i + j);
-        q[j] = bit >= 32 ? v[1] >> (bit - 32) : __funnelshift_r(v[0], v[1], bit);
-      }
-      r[i] = (q[0] & mask) | ((q[1] & mask) << 16) | magic;
+      for (int i = 0; i < 4; ++i)
+        r[i] = and_or<mask>(i < kFit ? a >> (F::kBits * i) : b >> (F::kBits * (i - kFit)), magic);
     }
   }
 }
@@ -602,6 +605,9 @@ struct Phase {
   static constexpr int kGu = F::kGs >= 32 ? F::kGs / 32 : 1;     // chunks per group
   static constexpr int kParts = F::template kHeld<1> / kGu;      // groups held, at most
   static constexpr int kArrays = F::kFp4 ? 1 : 2;
+  // The sums of x over groups of 32 would take 16 registers more than there are:
+  // they are made again with each row tile, by an MMA beside the codes'.
+  static constexpr bool kSumsInPlace = !F::kFp4 && kParts > 4;
   static constexpr float kOffset = code_offset<O, F>();
   static constexpr float kScale = product_scale<O, F>();
 
@@ -822,7 +828,7 @@ struct Phase {
   // to 4 pairs in a tile columns 0-3 hold the hi parts and 4-7 the lo parts of
   // one operand, else hi and lo are two operands.
   uint4 xv[F::template kHeld<PH> * PH];                       // of chunk c, operand b: c * NB + b
-  float sum[kParts][2];
+  float sum[kSumsInPlace ? 1 : kParts][2];
 
   template <int NB>
   __device__ __forceinline__ void load(int chunk) {
@@ -864,7 +870,7 @@ struct Phase {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           if constexpr (PH == 1) xv[c * NB + b] = order_x<F>(xv[c * NB + b]);
-          if constexpr (!F::kFp4) {
+          if constexpr (!F::kFp4 && !kSumsInPlace) {
             const uint4& v = xv[c * NB + b];
             constexpr uint32_t one = Op<O>::kOnes;
             Op<O>::mma(S, one, one, one, one, v.x, v.y, S[0], S[1], S[2], S[3]);
@@ -872,8 +878,10 @@ struct Phase {
           }
         }
       }
-      sum[k][0] = S[0] * (1.0f / kScale);
-      sum[k][1] = S[1] * (1.0f / kScale);
+      if constexpr (!kSumsInPlace) {
+        sum[k][0] = S[0] * (1.0f / kScale);
+        sum[k][1] = S[1] * (1.0f / kScale);
+      }
     }
   }
 
@@ -917,8 +925,9 @@ struct Phase {
         const uint4& v = xv[C * NB + b];
         const bool begin = b == 0 && (F::kGs == 16 || (half == 0 && C % kGu == 0));
         // a group starts from what takes the operand's offset off again
-        const float c0 = !begin ? P[0] : kOffset == 0.0f ? 0.0f : -kOffset * sum[k][0];
-        const float c1 = !begin ? P[1] : kOffset == 0.0f ? 0.0f : -kOffset * sum[k][1];
+        constexpr bool none = kOffset == 0.0f || kSumsInPlace;
+        const float c0 = !begin ? P[0] : none ? 0.0f : -kOffset * sum[kSumsInPlace ? 0 : k][0];
+        const float c1 = !begin ? P[1] : none ? 0.0f : -kOffset * sum[kSumsInPlace ? 0 : k][1];
         Op<O>::mma(P, lo[2 * half], hi[2 * half], lo[2 * half + 1], hi[2 * half + 1],
                    half ? v.z : v.x, half ? v.w : v.y, c0, c1, begin ? c0 : P[2], begin ? c1 : P[3]);
       }
@@ -931,11 +940,30 @@ struct Phase {
         tot[2] = fmaf(sh, P[2], tot[2]);
         tot[3] = fmaf(sh, P[3], tot[3]);
         if constexpr (!F::kFp4) {
-          const float bl = scale_in<kBias + o>(s), bh = scale_in<kBias + kHigh + o>(s);
-          tot[0] = fmaf(bl, sum[k][0], tot[0]);
-          tot[1] = fmaf(bl, sum[k][1], tot[1]);
-          tot[2] = fmaf(bh, sum[k][0], tot[2]);
-          tot[3] = fmaf(bh, sum[k][1], tot[3]);
+          float bl = scale_in<kBias + o>(s), bh = scale_in<kBias + kHigh + o>(s);
+          float x0, x1;
+          if constexpr (kSumsInPlace) {
+            // ones times 1 / kScale: 2^-24 is fp16's smallest number
+            constexpr uint32_t one = kScale == 1.0f ? Op<O>::kOnes : 0x00010001u;
+            float S[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const uint4& v = xv[C * NB + b];
+              Op<O>::mma(S, one, one, one, one, v.x, v.y, S[0], S[1], S[2], S[3]);
+              Op<O>::mma(S, one, one, one, one, v.z, v.w, S[0], S[1], S[2], S[3]);
+            }
+            x0 = S[0];
+            x1 = S[1];
+            bl = fmaf(-kOffset, sl, bl);
+            bh = fmaf(-kOffset, sh, bh);
+          } else {
+            x0 = sum[k][0];
+            x1 = sum[k][1];
+          }
+          tot[0] = fmaf(bl, x0, tot[0]);
+          tot[1] = fmaf(bl, x1, tot[1]);
+          tot[2] = fmaf(bh, x0, tot[2]);
+          tot[3] = fmaf(bh, x1, tot[3]);
         }
       }
     }
