@@ -65,10 +65,18 @@ struct RowScale {
 };
 __device__ __forceinline__ RowScale row_scale(float amax) {
   RowScale r;
-  r.s = __fdiv_rn(amax, 127.0f);
-  const bool finite = r.s <= 3.0e38f;                       // false for inf and NaN
-  r.how = !finite || r.s == 0.0f ? 0 : r.s < 1e-30f ? 2 : 1;
-  r.inv = r.how == 1 ? __fdiv_rn(1.0f, r.s) : 0.0f;
+  if (amax > 1e-28f && amax <= 3.4e38f) {
+    // amax / 127, correctly rounded: the rounded reciprocal's quotient corrected
+    // by its exact remainder (as for the codes below)
+    const float y = 1.0f / 127.0f, q = __fmul_rn(amax, y);
+    r.s = __fmaf_rn(__fmaf_rn(q, -127.0f, amax), y, q);
+    r.how = 1;
+    r.inv = __frcp_rn(r.s);
+  } else {
+    r.s = __fdiv_rn(amax, 127.0f);
+    r.how = r.s > 0.0f && r.s <= 3.4e38f ? 2 : 0;          // 0 for zero, inf and NaN
+    r.inv = 0.0f;
+  }
   return r;
 }
 __device__ __forceinline__ uint64_t pack2(float a, float b) {

@@ -77,6 +77,16 @@ def test_quantize_every_pattern(dt):
         check_quantize(to_dev(x[None]), dt)
 
 
+@pytest.mark.parametrize("dt", [0, 1])
+def test_quantize_every_maximum(dt):
+    """A row for every finite magnitude of the type, which is its largest."""
+    top = torch.arange(32768, dtype=torch.int32).to(torch.int16).view(TDT[dt])
+    top = top[torch.isfinite(top)]
+    x = top[:, None] * torch.linspace(-1, 1, 16).to(TDT[dt])[None, :]
+    x[:, 0] = -top
+    check_quantize(to_dev(x), dt)
+
+
 def codes(M, K, seed):
     return torch.randint(-128, 128, (M, K), dtype=torch.int8, generator=gen(seed)).to(DEV)
 
