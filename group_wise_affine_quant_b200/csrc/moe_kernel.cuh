@@ -29,7 +29,7 @@
 //
 // The codes become the A operand of mma.m16n8k16 as exact small numbers and x
 // the B operand; per group the products P and the sums X of x leave in fp32:
-//   sum += s P + b X,      P = sum (offset + q) x - offset X.
+//   sum += s P + (b - offset s) X,      P = sum (offset + q) x.
 // So w_hat is never rounded to T.  h is kept as two bf16 numbers (hi + lo, 16
 // bits of significand), in the B operand's order, so that down's operand
 // rounds far below T.  Each pair (token, slot) has its row of fp32 results;
@@ -924,12 +924,9 @@ struct Phase {
       for (int b = 0; b < NB; ++b) {
         const uint4& v = xv[C * NB + b];
         const bool begin = b == 0 && (F::kGs == 16 || (half == 0 && C % kGu == 0));
-        // a group starts from what takes the operand's offset off again
-        constexpr bool none = kOffset == 0.0f || kSumsInPlace;
-        const float c0 = !begin ? P[0] : none ? 0.0f : -kOffset * sum[kSumsInPlace ? 0 : k][0];
-        const float c1 = !begin ? P[1] : none ? 0.0f : -kOffset * sum[kSumsInPlace ? 0 : k][1];
         Op<O>::mma(P, lo[2 * half], hi[2 * half], lo[2 * half + 1], hi[2 * half + 1],
-                   half ? v.z : v.x, half ? v.w : v.y, c0, c1, begin ? c0 : P[2], begin ? c1 : P[3]);
+                   half ? v.z : v.x, half ? v.w : v.y, begin ? 0.0f : P[0], begin ? 0.0f : P[1],
+                   begin ? 0.0f : P[2], begin ? 0.0f : P[3]);
       }
       if (F::kGs == 16 || (half == 1 && (C + 1) % kGu == 0)) {
         constexpr int o = F::kGs == 16 ? 2 * C : k * F::kScaleSize;
@@ -940,7 +937,9 @@ struct Phase {
         tot[2] = fmaf(sh, P[2], tot[2]);
         tot[3] = fmaf(sh, P[3], tot[3]);
         if constexpr (!F::kFp4) {
-          float bl = scale_in<kBias + o>(s), bh = scale_in<kBias + kHigh + o>(s);
+          // the offset of the operand comes off with the bias
+          const float bl = fmaf(-kOffset, sl, scale_in<kBias + o>(s));
+          const float bh = fmaf(-kOffset, sh, scale_in<kBias + kHigh + o>(s));
           float x0, x1;
           if constexpr (kSumsInPlace) {
             // ones times 1 / kScale: 2^-24 is fp16's smallest number
@@ -954,8 +953,6 @@ struct Phase {
             }
             x0 = S[0];
             x1 = S[1];
-            bl = fmaf(-kOffset, sl, bl);
-            bh = fmaf(-kOffset, sh, bh);
           } else {
             x0 = sum[k][0];
             x1 = sum[k][1];
