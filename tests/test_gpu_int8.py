@@ -139,6 +139,35 @@ def test_int8_mm_many_tiles():
             api.lib().aq_testing_set_int8_plan(0, 0, 0)
 
 
+def sample(n, seed):
+    at = torch.randint(0, n, (40,), generator=gen(seed))
+    at[:2] = torch.tensor([0, n - 1])
+    return at.to(DEV)
+
+
+@pytest.mark.parametrize("N", [32768, 32769])
+def test_int8_mm_past_32_bits(N):
+    """More than 2^31 elements of y, and codes of x beyond 2^31 bytes; rows of y
+    by TMA and by the warps.  Checked at a sample of rows."""
+    for M, n, K in ((70000, N, 64), (140000, 64 + N % 2, 16384)):
+        xq = torch.randint(-128, 128, (M, K), dtype=torch.int8, device=DEV)
+        wq, xs, ws = codes(n, K, 3), scales(M, 3), scales(n, 4)
+        y = api.aq_int8_mm(xq, xs, wq, ws)
+        rows = sample(M, M)
+        assert torch.equal(y[rows], mm_ref(xq[rows], xs[rows], wq, ws, y.dtype))
+        del xq, y
+    assert api.lib().aq_device_errors() == 0
+
+
+def test_quantize_past_32_bits():
+    R, K = 70000, 32768
+    x = torch.randn((R, K), dtype=TDT[1], device=DEV)
+    q, s = api.aq_quantize_int8(x)
+    rows = sample(R, 9)
+    rq, rs = quantize_ref(dev_u16(x[rows]), 1)
+    assert np.array_equal(q[rows].cpu().numpy(), rq) and np.array_equal(s[rows].cpu().numpy(), rs)
+
+
 def test_int8_mm_largest_sum():
     """The longest K with the largest products: the 32-bit sum just fits."""
     K = 131056

@@ -258,6 +258,30 @@ def test_out_and_neighbours():
     errors()
 
 
+def test_offsets_past_32_bits():
+    """Experts that lie beyond 2^31 bytes of their stacks."""
+    E, H, I = 512, 4096, 2176
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+
+    def big(N, K):
+        q = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device=DEV, generator=g)
+        s = torch.rand((E, N, K // 128), device=DEV, generator=g).mul(0.01).to(TDT[1])
+        return q, s, (-8 * s.float()).to(TDT[1])
+    m = [big(I, H), big(I, H), big(H, I)]
+    assert m[0][0].numel() > 1 << 31
+    x = to_dev(normal((2, H), 1.0, 1, gen(2)))
+    indices = torch.tensor([[510, 0], [511, 7]], dtype=torch.int32, device=DEV)
+    weights = torch.full((2, 2), 0.5, device=DEV)
+    y = api.aq_moe_experts(x, indices, weights, *m, bits=4, group_size=128)
+    few = [tuple(t[[510, 0, 511, 7]].contiguous() for t in w) for w in m]
+    small = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device=DEV)
+    ref, tol = moe_ref.experts(u16_to_f64(dev_u16(x), 1), small.cpu().numpy(), weights.cpu().double().numpy(),
+                               *[host(w) for w in few], 4, 128, 1)
+    moe_ref.check(dev_u16(y), ref, tol, 1)
+    errors()
+
+
 def test_no_tokens():
     L = Layer(3, 64, 64, gs=32, seed=15)
     y, indices, weights = api.aq_moe(L.x(1)[:0], L.router, *L.m, 2, True, **L.kw)
