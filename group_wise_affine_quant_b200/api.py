@@ -396,8 +396,10 @@ def aq_quantize_int8(x, out=None):
 def aq_int8_mm(x_q, x_scales, w_q, w_scales, dtype=torch.bfloat16, out=None):
     """y [M, N] = dtype(x_q . w_q^T * x_scales[:, None] * w_scales[None, :]) for
     int8 x_q [M, K], w_q [N, K] and fp32 scales per token and channel."""
-    M, K = _matrix_shape("x_q", x_q)
-    N = _matrix_shape("w_q", w_q)[0]
+    xshape, wshape = x_q.shape, w_q.shape
+    if len(xshape) != 2 or len(wshape) != 2:
+        _matrix_shape("x_q", x_q), _matrix_shape("w_q", w_q)
+    (M, K), N = xshape, wshape[0]
     dev = x_q.get_device()
     if out is not None:
         dtype = out.dtype
@@ -405,8 +407,12 @@ def aq_int8_mm(x_q, x_scales, w_q, w_scales, dtype=torch.bfloat16, out=None):
     if dt is None:
         raise TypeError("expected fp16 or bf16 as the result's type, got %s" % dtype)
     i8, f32 = torch.int8, torch.float32
-    if not (dev >= 0 and _fits(x_q, i8, (M, K), dev) and _fits(w_q, i8, (N, K), dev)
-            and _fits(x_scales, f32, (M,), dev) and _fits(w_scales, f32, (N,), dev)):
+    # _fits of the four, written out
+    if not (dev >= 0 and wshape[1] == K and x_scales.shape == (M,) and w_scales.shape == (N,)
+            and x_q.dtype is i8 and w_q.dtype is i8 and x_scales.dtype is f32 and w_scales.dtype is f32
+            and x_q.is_contiguous() and w_q.is_contiguous() and x_scales.is_contiguous()
+            and w_scales.is_contiguous() and w_q.get_device() == dev and x_scales.get_device() == dev
+            and w_scales.get_device() == dev):
         _refuse(x_q, ("x_q", x_q, i8, (M, K)), ("x_scales", x_scales, f32, (M,)),
                 ("w_q", w_q, i8, (N, K)), ("w_scales", w_scales, f32, (N,)))
     if out is None:
@@ -426,11 +432,15 @@ def aq_int8_mm(x_q, x_scales, w_q, w_scales, dtype=torch.bfloat16, out=None):
 def aq_qqmm_int8(x, w_q, w_scales, out=None, workspace=None):
     """W8A8: y [M, N] = x . w^T with the rows of x [M, K] fp16/bf16 quantized on
     the way and an int8 weight w_q [N, K] with fp32 scales per channel."""
-    M, K = _matrix_shape("x", x)
-    N = _matrix_shape("w_q", w_q)[0]
+    xshape, wshape = x.shape, w_q.shape
+    if len(xshape) != 2 or len(wshape) != 2:
+        _matrix_shape("x", x), _matrix_shape("w_q", w_q)
+    (M, K), N = xshape, wshape[0]
     dt, dev = _dt(x), x.get_device()
-    if not (dev >= 0 and x.is_contiguous() and _fits(w_q, torch.int8, (N, K), dev)
-            and _fits(w_scales, torch.float32, (N,), dev)):
+    # _fits of the three, written out
+    if not (dev >= 0 and wshape[1] == K and w_scales.shape == (N,) and w_q.dtype is torch.int8
+            and w_scales.dtype is torch.float32 and x.is_contiguous() and w_q.is_contiguous()
+            and w_scales.is_contiguous() and w_q.get_device() == dev and w_scales.get_device() == dev):
         _refuse(x, ("x", x, x.dtype, (M, K)), ("w_q", w_q, torch.int8, (N, K)),
                 ("w_scales", w_scales, torch.float32, (N,)))
     if out is None:
