@@ -82,7 +82,7 @@ struct Format {
   static constexpr Order kOrder = GS == 16 ? Order::kGroup16 : BITS == 8 ? Order::kPairs : Order::kSplit;
   static constexpr int kScaleSize = FP4 ? 1 : 2;
   // 32-chunks of x a warp holds with NB operands each: what the registers take,
-  // and what lets two stages of 16 warps' chunks fit the ring.
+  // and what lets three stages of its rows fit a warp's ring.
   template <int NB> static constexpr int kHeld = BITS <= 4 ? 8 / NB : 4;
   // A stage of a warp: its part of 16 rows.  A copied window starts at the 16
   // bytes (codes; rows start at multiples of 4 bytes, of 16 for 4 and 8 bits)
@@ -740,7 +740,7 @@ struct Phase {
   __device__ __forceinline__ int row0(int tl, int rb) const {
     return plan.tile_expert[tl] * (PH == 1 ? p.a.I : p.a.H) + rb * kRows;
   }
-  // Row tile j of a batch is team j % teams'; a team has up to 2.
+  // Row tile j of a batch is team j % teams'; a team has up to kBatch.
   __device__ __forceinline__ int mine(const Cursor& c) const {
     return min(kBatch, (c.nb - team + (1 << lt) - 1) >> lt);
   }
