@@ -16,7 +16,7 @@
 // Work is cut into row tiles of 16 rows (8 gate rows and the same 8 up rows, so
 // that both factors of h meet in one place, or 16 down rows) times a token tile,
 // up to 4 or 8 of the tokens that chose the expert.  A CTA takes neighbouring row
-// tiles; a team of 4, 8 or 16 of its warps shares the K of one, so each warp
+// tiles; a team of 2 to 16 of its warps shares the K of one, so each warp
 // keeps its part of x in registers over all row tiles of a token tile and
 // streams its part of the weight rows by cp.async through a ring of its own.
 // The warps' sums meet in shared memory after four row tiles per team (with two
@@ -53,7 +53,6 @@ constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxPairs = 1024;          // tokens * top_k
 constexpr int kMaxExperts = 512;
-constexpr int kMaxTopK = 16;
 constexpr int kBatch = 4;                // row tiles of a team between two barriers (even)
 constexpr int kExchangeLanes = 33;       // a lane more, to spread the banks
 constexpr int kCounterBytes = 65536;     // the workspace's shared counter area
@@ -658,7 +657,7 @@ struct Phase {
   // log2 of the teams: as few warps to a team as hold K, but no more teams than
   // pairs of row tiles.
   static __device__ __forceinline__ int teams_of(int chunks, int held, int tiles) {
-    int lt = chunks <= 4 * held ? 2 : chunks <= 8 * held ? 1 : 0;
+    int lt = chunks <= 2 * held ? 3 : chunks <= 4 * held ? 2 : chunks <= 8 * held ? 1 : 0;
     while (lt > 0 && tiles <= 1 << lt) --lt;
     return lt;
   }
@@ -702,9 +701,9 @@ struct Phase {
     open();
     own = exchange + (warp * kExchangeLanes + lane) * 16;
     {
-      // 64 pairs of numbers per row tile, each by 4 / teams lanes that add four
-      // warps' each
-      const int spread = 2 - lt, item = (warp << (5 - spread)) + (lane >> spread);
+      // 64 pairs of numbers per row tile, each by 4 / teams lanes (one from 4
+      // teams on) that add up to four warps' each
+      const int spread = max(2 - lt, 0), item = (warp << (5 - spread)) + (lane >> spread);
       const int src = (item >> 1) & 31, part = lane & ((1 << spread) - 1);
       jtile = item >> 6;
       jcol = 2 * (src & 3) + (item & 1);
@@ -980,7 +979,7 @@ struct Phase {
   // warps of each team.
   __device__ __forceinline__ void join(int rb, int nb, int first, int count) {
 #pragma unroll 1
-    for (int i = 0; i < kBatch && i << lt < nb; i += 2) {
+    for (int i = 0; i < kBatch && i << lt < nb; i += lt == 3 ? 1 : 2) {
       const int jt = jtile + (i << lt);
       const bool live = (jt & 63) < nb;
       float a = 0.0f, b = 0.0f;
@@ -988,6 +987,7 @@ struct Phase {
         const uint32_t o = others + (turn & 1) * kBuffer + i * (kWarps * kExchangeLanes * 16);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
+          if (lt == 3 && m >= 2) break;
           const float2 v = lds_f2(o + m * (kExchangeLanes * 16));
           a += v.x;
           b += v.y;
@@ -1002,8 +1002,8 @@ struct Phase {
         }
       }
       if (PH == 2 && count <= 4) {                       // columns of hi and lo
-        a += __shfl_down_sync(0xFFFFFFFFu, a, 16 >> lt);
-        b += __shfl_down_sync(0xFFFFFFFFu, b, 16 >> lt);
+        a += __shfl_down_sync(0xFFFFFFFFu, a, max(16 >> lt, 4));
+        b += __shfl_down_sync(0xFFFFFFFFu, b, max(16 >> lt, 4));
       }
       if (jt < nb && jcol < count) store(a, b, plan.order[first + jcol], rb + jt, jrow);
     }

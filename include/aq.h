@@ -410,7 +410,7 @@ typedef struct aq_moe_matrix {
  * aq_moe — a whole mixture-of-experts layer for a few tokens, in one launch
  * (the serving step around the products that aq_gather_qmm gives for indices
  * known on the host).  Per token x [H]:
- *   l = x . w_router^T                 (exact products, fp64 sums)
+ *   l = x . w_router^T                 (fp32 products, exact in its range; fp64 sums)
  *   the top_k experts by l (ties: the lower index), p = softmax(l) over all E
  *   weight = p_e, or with `normalize` p_e / sum of the chosen p
  *   h_e = silu(x . gate_e^T) * (x . up_e^T),   silu(v) = v / (1 + exp(-v))
