@@ -10,6 +10,7 @@ take stacks [E, ...] of the same weights.
 """
 import ctypes
 import functools
+import threading
 
 import torch
 
@@ -329,15 +330,26 @@ def _matrix_shape(name, t):
     return t.shape
 
 
-_scratch = {}
+class _Scratch(threading.local):
+    """Default scratch of the calling host thread, a buffer per device and
+    stream.  Threads do not share one, though they share the default stream: a
+    call may be several launches, and another thread's may come between them."""
+
+    def __init__(self):
+        self.bufs = {}
+
+
+_scratch = _Scratch()
 
 
 def _workspace(workspace, x, nbytes, counters):
-    """(address, bytes) of the caller's Workspace, or of a buffer of this device
-    and stream (calls on two streams may overlap); a call that is being captured
-    gets one of its own, which lives in the graph's memory."""
+    """(buffer, address, bytes) of the caller's Workspace, or of a buffer of this
+    host thread, device and stream (calls on two streams may overlap); a call
+    that is being captured gets one of its own, which lives in the graph's
+    memory.  The caller holds the buffer until it has launched: the address alone
+    does not keep it from the allocator."""
     if nbytes == 0:
-        return None, 0
+        return None, None, 0
     if workspace is not None:
         buf = workspace.get(x.device, nbytes)
     elif torch.cuda.is_current_stream_capturing():
@@ -347,10 +359,11 @@ def _workspace(workspace, x, nbytes, counters):
     else:
         dev = x.get_device()
         key = (dev, _stream_of(dev))
-        buf = _scratch.get(key)
+        bufs = _scratch.bufs
+        buf = bufs.get(key)
         if buf is None or buf.numel() < nbytes:
-            buf = _scratch[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=x.device)
-    return buf.data_ptr(), buf.numel()
+            buf = bufs[key] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=x.device)
+    return buf, buf.data_ptr(), buf.numel()
 
 
 _COUNTER_BYTES = 65536           # at a workspace's start, zero between calls (include/aq.h)
@@ -431,7 +444,8 @@ def aq_int8_mm(x_q, x_scales, w_q, w_scales, dtype=torch.bfloat16, out=None):
 
 def aq_qqmm_int8(x, w_q, w_scales, out=None, workspace=None):
     """W8A8: y [M, N] = x . w^T with the rows of x [M, K] fp16/bf16 quantized on
-    the way and an int8 weight w_q [N, K] with fp32 scales per channel."""
+    the way and an int8 weight w_q [N, K] with fp32 scales per channel.  A
+    `workspace` passed in serves one host thread and stream at a time."""
     xshape, wshape = x.shape, w_q.shape
     if len(xshape) != 2 or len(wshape) != 2:
         _matrix_shape("x", x), _matrix_shape("w_q", w_q)
@@ -450,7 +464,7 @@ def aq_qqmm_int8(x, w_q, w_scales, out=None, workspace=None):
     if dev != _current_device():
         with torch.cuda.device(dev):
             return aq_qqmm_int8(x, w_q, w_scales, out, workspace)
-    ws, nbytes = _workspace(workspace, x, _qqmm_int8_bytes(M, N, K), False)
+    buf, ws, nbytes = _workspace(workspace, x, _qqmm_int8_bytes(M, N, K), False)
     st = lib().aq_qqmm_int8(x.data_ptr(), w_q.data_ptr(), w_scales.data_ptr(), out.data_ptr(), M, N, K, dt,
                             ws, nbytes, _stream_of(dev))
     if st:
@@ -528,7 +542,7 @@ def aq_moe(x, w_router, gate, up, down, top_k, normalize=True, bits=4, group_siz
     k = max(int(top_k), 0)
     indices = torch.empty(T, k, dtype=torch.int32, device=x.device)
     weights = torch.empty(T, k, dtype=torch.float32, device=x.device)
-    ws, nbytes = _workspace(workspace, x, _moe_bytes(T, H, I, E, k), True)
+    buf, ws, nbytes = _workspace(workspace, x, _moe_bytes(T, H, I, E, k), True)
     m = _Nine(*at)
     a = ctypes.addressof(m)
     st = _by_address("aq_moe")(x.data_ptr(), w_router.data_ptr(), a, a + 24, a + 48, out.data_ptr(),
@@ -553,7 +567,7 @@ def aq_moe_experts(x, indices, weights, gate, up, down, bits=4, group_size=64, o
     if dev != _current_device():
         with torch.cuda.device(dev):
             return aq_moe_experts(x, indices, weights, gate, up, down, bits, group_size, out, workspace)
-    ws, nbytes = _workspace(workspace, x, _moe_bytes(T, H, I, E, k), True)
+    buf, ws, nbytes = _workspace(workspace, x, _moe_bytes(T, H, I, E, k), True)
     m = _Nine(*at)
     a = ctypes.addressof(m)
     st = _by_address("aq_moe_experts")(x.data_ptr(), indices.data_ptr(), weights.data_ptr(), a, a + 24, a + 48,

@@ -392,7 +392,9 @@ AQ_API aq_status aq_int8_mm(const void* x_q, const float* x_scales, const void* 
  * weight loads start while x is quantized).  x [M, K] T, 16-byte aligned; the
  * rest as aq_int8_mm.  Workspace: aq_workspace_size(AQ_OP_QQMM_INT8, M, N, K,
  * 8, 16, AQ_MODE_AFFINE, 1) bytes, 256-byte aligned; its first 64 KB are left
- * as they are, so the buffer may be one that serves the other calls.
+ * as they are, so the buffer may be one that serves the other calls of a host
+ * thread.  Host threads need a buffer each even on one stream: another
+ * thread's launch may come between the two of a call.
  */
 AQ_API aq_status aq_qqmm_int8(const void* x, const void* w_q, const float* w_scales, void* y,
                               int64_t M, int64_t N, int64_t K, aq_dtype dtype, void* workspace,
