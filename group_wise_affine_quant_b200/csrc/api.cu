@@ -847,8 +847,8 @@ int aq_testing_gather_groups(const int32_t* lhs_indices, const int32_t* rhs_indi
   return gg.G;
 }
 
-void aq_testing_set_wait_limit_ns(uint64_t ns) { aq::testing_set_mv_wait_ns(ns); }
-void aq_testing_set_start_delay_ns(uint64_t ns) { aq::testing_set_mv_delay_ns(ns); }
+void aq_testing_set_wait_limit_ns(uint64_t ns) { aq::testing_set_wait_ns(ns); }
+void aq_testing_set_start_delay_ns(uint64_t ns) { aq::testing_set_delay_ns(ns); }
 void aq_testing_set_int8_plan(int tokens, int pair, int splits) {
   aq::testing_set_int8_plan(tokens, pair, splits);
 }
@@ -857,6 +857,7 @@ aq_status aq_testing_clear_device_errors(void) {
   g_err[0] = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = aq::testing_clear_device_error_qmv_mma();
+  if (e == cudaSuccess) e = aq::testing_clear_device_error_moe();
   return cuda_status(e, "aq_testing_clear_device_errors");
 }
 

@@ -91,9 +91,12 @@ cudaError_t launch_qmv_mma(const void* x, const void* w_q, const void* scales,
 cudaError_t launch_qmv_mma_batched(const QmvProblemDesc* probs, int count, int64_t M, int gs,
                                    int dtype, void* ws, cudaStream_t st);
 cudaError_t read_device_error_qmv_mma(unsigned* out);
-// Test hooks of the warp-MMA decode kernel (aq_testing.h).
-void testing_set_mv_wait_ns(uint64_t ns);
-void testing_set_mv_delay_ns(uint64_t ns);
+// Test hooks (aq_testing.h): the bound of a kernel's waits and the delay of its
+// start, for launches from now on, and what was set (the bound: 2 s if nothing).
+void testing_set_wait_ns(uint64_t ns);
+void testing_set_delay_ns(uint64_t ns);
+uint64_t testing_wait_ns();
+uint64_t testing_delay_ns();
 cudaError_t testing_clear_device_error_qmv_mma();
 // Launches the warp-MMA decode kernel on that scratch.  Sets *need to the
 // scratch bytes the shape needs; returns cudaErrorMemoryAllocation (nothing
@@ -145,4 +148,5 @@ struct MoeArgs {
 size_t moe_workspace(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k);
 cudaError_t launch_moe(const MoeArgs& a, int bits, int mode, int dtype, cudaStream_t st);
 cudaError_t read_device_error_moe(unsigned* out);
+cudaError_t testing_clear_device_error_moe();
 }  // namespace aq

@@ -50,6 +50,8 @@ cudaError_t launch_moe(const MoeArgs& a, int bits, int mode, int dtype, cudaStre
   int sms = 0;
   cudaError_t e = device_of(&sms, &p.error);
   if (e != cudaSuccess) return e;
+  p.wait_ns = testing_wait_ns();
+  p.delay_ns = testing_delay_ns();
   const int64_t pairs = (int64_t)a.T * a.top_k;
   p.a = a;
   p.bars = reinterpret_cast<unsigned*>(a.workspace);
@@ -73,6 +75,10 @@ cudaError_t launch_moe(const MoeArgs& a, int bits, int mode, int dtype, cudaStre
 
 cudaError_t read_device_error_moe(unsigned* out) {
   return cudaMemcpyFromSymbol(out, g_moe_device_error, sizeof(unsigned));
+}
+cudaError_t testing_clear_device_error_moe() {
+  const unsigned z = 0;
+  return cudaMemcpyToSymbol(g_moe_device_error, &z, sizeof(z));
 }
 
 }  // namespace aq

@@ -56,7 +56,6 @@ constexpr int kMaxExperts = 512;
 constexpr int kBatch = 4;                // row tiles of a team between two barriers (even)
 constexpr int kExchangeLanes = 33;       // a lane more, to spread the banks
 constexpr int kCounterBytes = 65536;     // the workspace's shared counter area
-constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct Params {
   MoeArgs a;
@@ -65,6 +64,8 @@ struct Params {
   float* part;                           // [pairs][H]
   unsigned* bars;                        // grid barrier counters (zero between calls)
   unsigned* error;
+  uint64_t wait_ns;                      // bound of a wait at a grid barrier
+  uint64_t delay_ns;                     // test hook: start delay of one CTA (0: none)
 };
 
 // ------------------------------------------------------------ code operands
@@ -354,14 +355,14 @@ __device__ __forceinline__ void grid_arrive(unsigned* counter) {
   if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
 }
 // Until every CTA has arrived; false after the time limit.
-__device__ __forceinline__ bool grid_wait(unsigned* counter, unsigned ctas, int* abort) {
+__device__ __forceinline__ bool grid_wait(unsigned* counter, unsigned ctas, int* abort, uint64_t wait_ns) {
   if (threadIdx.x == 0) {
     const uint64_t t0 = globaltimer_ns();
     for (unsigned it = 1;; ++it) {
       unsigned v;
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
       if (v >= ctas) break;
-      if ((it & 255u) == 0u && globaltimer_ns() - t0 > kWaitNs) {
+      if ((it & 255u) == 0u && globaltimer_ns() - t0 > wait_ns) {
         *abort = 1;
         break;
       }
@@ -1129,7 +1130,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t exchange = smem_u32(smem) + kExchangeAt;
   const uint32_t ring = smem_u32(smem) + kRingAt + warp * kRingBytes;
-  if (threadIdx.x == 0) plan.abort = 0;
+  if (threadIdx.x == 0) {
+    plan.abort = 0;
+    if (p.delay_ns && blockIdx.x == 0) {                 // test hook
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < p.delay_ns) {
+      }
+    }
+  }
 
   // The grid's row tiles are cut at these fractions of 2^32 (the last CTA ends
   // with the last tile).
@@ -1141,7 +1149,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   if (p.a.w_router) {
     router_logits<T>(p, warp, lane);
     grid_arrive(p.bars + 0);
-    ok = grid_wait(p.bars + 0, gridDim.x, &plan.abort);
+    ok = grid_wait(p.bars + 0, gridDim.x, &plan.abort, p.wait_ns);
     if (ok) choose(p, plan, warp, lane);
   } else {
     for (int q = threadIdx.x; q < p.a.T * p.a.top_k; q += kThreads) {
@@ -1166,20 +1174,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     Down down(p, plan, ring, exchange, warp, lane, Down::border(p, plan, share),
               last ? plan.tiles * Down::blocks_of(p) : Down::border(p, plan, share + step));
     down.start();
-    ok = grid_wait(p.bars + 1, gridDim.x, &plan.abort);
+    ok = grid_wait(p.bars + 1, gridDim.x, &plan.abort, p.wait_ns);
     if (ok) {
       down.run();
       grid_arrive(p.bars + 2);
-      ok = grid_wait(p.bars + 2, gridDim.x, &plan.abort);
+      ok = grid_wait(p.bars + 2, gridDim.x, &plan.abort, p.wait_ns);
       if (ok) weighted_sums<T>(p, plan);
     }
   }
   cp_wait<0>();
   if (threadIdx.x == 0) {
+    // Every CTA comes by here, one that gave up too: the last leaves the counters
+    // at zero, so that a time-out does not spoil the calls to come.  Who has
+    // passed all barriers has seen all arrivals; the fences order those of CTAs
+    // that gave up before the zeros.
     if (!ok) {
       atomicOr(p.error, 1u);
-    } else if (atomicAdd(p.bars + 3, 1u) == gridDim.x - 1) {
-      // every CTA is past the last barrier: the counters are zero again
+      __threadfence();
+    }
+    if (atomicAdd(p.bars + 3, 1u) == gridDim.x - 1) {
+      if (!ok) __threadfence();
       p.bars[0] = p.bars[1] = p.bars[2] = p.bars[3] = 0u;
     }
   }

@@ -698,8 +698,8 @@ qmv_mma_kernel(const __grid_constant__ MvParams<P> pr) {
 }
 
 // ------------------------------------------------------------------- host
-// Test hooks (aq_testing.h): wait bound and TMA-warp start delay, in ns.
-std::atomic<uint64_t> g_mv_wait_ns{0}, g_mv_delay_ns{0};
+// Test hooks (aq_testing.h): wait bound and start delay, in ns.
+std::atomic<uint64_t> g_wait_ns{0}, g_delay_ns{0};
 
 struct MvSplit {
   int splits, kslice;
@@ -847,9 +847,8 @@ cudaError_t mv_launch_group(const QmvProblemDesc* probs, int count, int64_t M, v
   pr.M = (int)M;
   pr.weights_early = weight_prefetch_enabled();
   pr.ws = reinterpret_cast<uint32_t*>(ws);
-  const uint64_t wl = g_mv_wait_ns.load(std::memory_order_relaxed);
-  pr.wait_ns = wl ? wl : 2000000000ull;
-  pr.delay_ns = g_mv_delay_ns.load(std::memory_order_relaxed);
+  pr.wait_ns = testing_wait_ns();
+  pr.delay_ns = testing_delay_ns();
   const int grid = std::min(units, slots);
   return MvKernel<T, GS, NT, P>::launch(pr, grid, st);
 }
@@ -925,8 +924,13 @@ cudaError_t launch_qmv_mma_batched(const QmvProblemDesc* probs, int count, int64
 
 cudaError_t read_device_error_qmv_mma(unsigned* out) { return read_tu_error(out); }
 
-void testing_set_mv_wait_ns(uint64_t ns) { g_mv_wait_ns.store(ns, std::memory_order_relaxed); }
-void testing_set_mv_delay_ns(uint64_t ns) { g_mv_delay_ns.store(ns, std::memory_order_relaxed); }
+void testing_set_wait_ns(uint64_t ns) { g_wait_ns.store(ns, std::memory_order_relaxed); }
+void testing_set_delay_ns(uint64_t ns) { g_delay_ns.store(ns, std::memory_order_relaxed); }
+uint64_t testing_wait_ns() {
+  const uint64_t ns = g_wait_ns.load(std::memory_order_relaxed);
+  return ns ? ns : 2000000000ull;
+}
+uint64_t testing_delay_ns() { return g_delay_ns.load(std::memory_order_relaxed); }
 cudaError_t testing_clear_device_error_qmv_mma() {
   const unsigned z = 0;
   return cudaMemcpyToSymbol(g_aq_device_error, &z, sizeof(z));

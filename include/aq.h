@@ -430,7 +430,8 @@ typedef struct aq_moe_matrix {
  * The kernel is launched cooperatively (its steps meet at grid barriers) and
  * holds every SM: a call on another stream runs before or after it.
  * Workspace: aq_moe_workspace_size bytes, under aq_qmv's rules (zero-filled
- * before its first use; calls that may overlap need separate buffers).
+ * before its first use; calls that may overlap need separate buffers).  The
+ * counters are zero again after a call that timed out, too.
  */
 AQ_API aq_status aq_moe(const void* x, const void* w_router, const aq_moe_matrix* gate,
                         const aq_moe_matrix* up, const aq_moe_matrix* down, void* y,
@@ -469,8 +470,8 @@ AQ_API size_t aq_workspace_size(aq_op op, int64_t M, int64_t N, int64_t K, int b
 /*
  * Device-side error bits accumulated since the library was loaded on the
  * current device (0 = none).  Bit 0: a kernel's bounded wait on an mbarrier
- * timed out (after 2 s); the kernel stopped, freed its tensor memory and left
- * its output incomplete.  Synchronises with the device (reads a __device__
+ * or a grid barrier timed out (after 2 s); the kernel stopped, freed its
+ * tensor memory and left its output incomplete.  Synchronises with the device (reads a __device__
  * variable).  Returns 0xFFFFFFFF if the read itself fails.
  */
 AQ_API unsigned aq_device_errors(void);

@@ -1,15 +1,16 @@
 /*
  * aq_testing.h — test hooks of libaq (not for production use).
  *
- * They let a test drive the failure path of the decode kernels' bounded waits
- * (the bound every mbarrier wait of a kernel has, after which the kernel stops
+ * They let a test drive the failure path of a kernel's bounded waits (the
+ * bound every mbarrier or grid-barrier wait has, after which the kernel stops
  * issuing work, lets its copies in flight land, sets bit 0 of
  * aq_device_errors() and returns) without faulting the GPU: the host shortens
  * the bound and delays one role of the kernel past it, so that the waits of
  * the other roles run out.  The pages have no counterpart.
  *
- * Scope: the warp-MMA decode kernel behind aq_qmv / aq_qmv_batched /
- * aq_qmv_noalloc (4-bit affine weights), aq_qmv's kernel choice,
+ * Scope: the bounded waits of the warp-MMA decode kernel behind aq_qmv /
+ * aq_qmv_batched / aq_qmv_noalloc (4-bit affine weights) and of the
+ * mixture-of-experts kernel; aq_qmv's kernel choice,
  * aq_gather_qmm's grouping of index pairs, and aq_int8_mm's tile.  The
  * settings are process-wide and apply to launches made after the call; 0
  * restores the default.
@@ -23,11 +24,12 @@
 extern "C" {
 #endif
 
-/* Bound of every mbarrier wait of the decode kernel, in ns (default 2 s). */
+/* Bound of every wait of these kernels, in ns (default 2 s). */
 AQ_API void aq_testing_set_wait_limit_ns(uint64_t ns);
 
-/* Delay, in ns, before the decode kernel's TMA warp issues its first copy
- * (default 0).  The delay ends early once another role has given up. */
+/* Delay, in ns, before the decode kernel's TMA warp issues its first copy, or
+ * before one CTA of the mixture-of-experts kernel starts (default 0).  The
+ * former ends early once another role has given up. */
 AQ_API void aq_testing_set_start_delay_ns(uint64_t ns);
 
 /* Kernel that later aq_qmv calls of this process use where it applies:
@@ -55,8 +57,8 @@ AQ_API int aq_testing_gather_groups(const int32_t* lhs_indices, const int32_t* r
                                     int64_t x_batch, int32_t* xmap, int32_t* ymap,
                                     int64_t map_rows, int* rows_per_group);
 
-/* Clears the device error bits that aq_device_errors() reports.  Synchronises
- * the current device first. */
+/* Clears the device error bits that these kernels have set.  Synchronises the
+ * current device first. */
 AQ_API aq_status aq_testing_clear_device_errors(void);
 
 #ifdef __cplusplus
