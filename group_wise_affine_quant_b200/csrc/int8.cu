@@ -517,7 +517,10 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
       if (!ok) {
         // Gave up: the MMAs issued end before the TMEM is freed.
         int ignore = 0;
-        if (elect_one()) mma_commit(drain);
+        if (elect_one()) {
+          if constexpr (PAIR) mma_commit_pair(drain);
+          else mma_commit(drain);
+        }
         __syncwarp();
         mbar_wait(drain, 0, &ignore, 200000000ull);
       }
