@@ -857,6 +857,7 @@ aq_status aq_testing_clear_device_errors(void) {
   g_err[0] = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = aq::testing_clear_device_error_qmv_mma();
+  if (e == cudaSuccess) e = aq::testing_clear_device_error_int8();
   if (e == cudaSuccess) e = aq::testing_clear_device_error_moe();
   return cuda_status(e, "aq_testing_clear_device_errors");
 }

@@ -259,7 +259,15 @@ struct MmArgs {
   int m_tiles, n_tiles;
   int prefetch;          // weights may be read before the previous kernel has ended
   int tma_out;           // y's rows suit TMA (N a multiple of 8)
+  uint64_t wait_ns;      // bound of every mbarrier wait
+  uint64_t delay_ns;     // test hook: TMA warp start delay (0: none)
 };
+
+// Sets the flag at this shared-memory offset in another CTA of the cluster.
+__device__ __forceinline__ void raise_remote(uint32_t cluster_addr) {
+  asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(cluster_addr) : "memory");
+}
+constexpr uint64_t kDrainNs = 200000000ull;   // bound of the waits after giving up
 
 __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t acc) {
@@ -367,7 +375,11 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
   auto tfull = [&](int b) { return bars + 8u * (2 * ST + b); };
   auto tempty = [&](int b) { return bars + 8u * (2 * ST + 2 + b); };
   const uint32_t drain = bars + 8u * (2 * ST + 4);
-
+  // A role that gives up ends its CTA's waits by the flag, and the other CTA's
+  // of a pair by that one's: neither can finish alone.
+  auto tell_peer = [&]() {
+    if constexpr (PAIR) raise_remote(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), cluster_rank() ^ 1u));
+  };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool clustered = PAIR || a.splits > 1;
   const uint32_t rank = clustered ? cluster_rank() : 0u;
@@ -409,6 +421,7 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
   const int kb0 = PAIR ? 0 : (int)rank * a.kb_split;
   const int nkb = PAIR ? a.kblocks : min(a.kb_split, a.kblocks - kb0);   // > 0 by the plan
   constexpr int kRowsA = PAIR ? 2 * kBM : kBM;           // rows of the A operand per tile
+  uint32_t issued = 0;                                   // stages the TMA warp has asked for
 
   if (warp == 0) {
     // ------------------------------------------------------------- TMA warp
@@ -442,13 +455,19 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
       __syncwarp();
     }
     pdl_wait();
+    if (a.delay_ns) {                                    // test hook
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < a.delay_ns && !*abort_flag) {
+      }
+      __syncwarp();
+    }
     for (int t = first; t < tiles && ok; t += step) {
       int mt, nt;
       tile_at(t, a.m_tiles, a.n_tiles, mt, nt);
       for (int k = 0; k < nkb; ++k, ++it) {
         const int s = (int)(it % ST);
         const bool early = it < (uint32_t)pre;
-        if (!mbar_wait(empty(s), ((it / ST) & 1u) ^ 1u, abort_flag)) {
+        if (!mbar_wait(empty(s), ((it / ST) & 1u) ^ 1u, abort_flag, a.wait_ns)) {
           ok = false;
           break;
         }
@@ -462,15 +481,8 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
         __syncwarp();
       }
     }
-    if (!ok && leader) {
-      // Gave up: the copies in flight land before the CTA may exit.
-      int ignore = 0;
-      const uint32_t n = it < (uint32_t)ST ? it : (uint32_t)ST;
-      for (uint32_t j = 0; j < n; ++j) {
-        const uint32_t i = it - 1 - j;
-        mbar_wait(full((int)(i % ST)), (i / ST) & 1u, &ignore, 200000000ull);
-      }
-    }
+    issued = it;
+    if (!ok) tell_peer();
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA warp
     if (leader) {
@@ -480,14 +492,14 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
       for (int t = first; t < tiles && ok; t += step, ++tile_i) {
         const int b = (int)(tile_i & 1u);
         const uint32_t use = tile_i >> 1;
-        ok = PAIR ? mbar_wait_cluster(tempty(b), (use & 1u) ^ 1u, abort_flag)
-                  : mbar_wait(tempty(b), (use & 1u) ^ 1u, abort_flag);
+        ok = PAIR ? mbar_wait_cluster(tempty(b), (use & 1u) ^ 1u, abort_flag, a.wait_ns)
+                  : mbar_wait(tempty(b), (use & 1u) ^ 1u, abort_flag, a.wait_ns);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(b * BN);
         for (int k = 0; k < nkb; ++k, ++it) {
           const int s = (int)(it % ST);
-          if (!mbar_wait(full(s), (it / ST) & 1u, abort_flag)) {
+          if (!mbar_wait(full(s), (it / ST) & 1u, abort_flag, a.wait_ns)) {
             ok = false;
             break;
           }
@@ -516,13 +528,14 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
       }
       if (!ok) {
         // Gave up: the MMAs issued end before the TMEM is freed.
+        tell_peer();
         int ignore = 0;
         if (elect_one()) {
           if constexpr (PAIR) mma_commit_pair(drain);
           else mma_commit(drain);
         }
         __syncwarp();
-        mbar_wait(drain, 0, &ignore, 200000000ull);
+        mbar_wait(drain, 0, &ignore, kDrainNs);
       }
     }
   } else {
@@ -563,7 +576,7 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
       named_barrier_sync(1, kEt);
       ask(t + step);
       // after giving up the warps still meet at the barrier above
-      if (ok) ok = mbar_wait(tfull(b), (tile_i >> 1) & 1u, abort_flag);
+      if (ok) ok = mbar_wait(tfull(b), (tile_i >> 1) & 1u, abort_flag, a.wait_ns);
       if (!ok) continue;
       tc_fence_after();
       const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN);
@@ -706,6 +719,7 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
         if (lane == 0) mbar_arrive(tempty(b));
       }
     }
+    if (!ok) tell_peer();
     if (PAIR && lane == 0) bulk_wait_all();              // y is written, the buffers are free
   }
 
@@ -764,7 +778,31 @@ int8_mm_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ C
     cluster_wait();
   }
   __syncthreads();
-  if (threadIdx.x == 0 && *abort_flag) atomicOr(&g_int8_device_error, 1u);
+  if (*abort_flag) {
+    // Gave up (both CTAs of a pair know by now).  The copies in flight land before
+    // a CTA exits, also those that the TMA warp asked for without waiting for
+    // anything later.
+    if (warp == 0 && leader) {
+      int ignore = 0;
+      const uint32_t n = issued < (uint32_t)ST ? issued : (uint32_t)ST;
+      for (uint32_t j = 0; j < n; ++j) {
+        const uint32_t i = issued - 1 - j;
+        mbar_wait(full((int)(i % ST)), (i / ST) & 1u, &ignore, kDrainNs);
+      }
+    } else if (warp == 0) {
+      // A stage that the leader did not ask for completes on no barrier: 10 ms
+      // are a thousand times as long as a copy takes.
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 10000000ull) {
+      }
+    }
+    if (PAIR) {
+      cluster_arrive();
+      cluster_wait();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) atomicOr(&g_int8_device_error, 1u);
+  }
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR) tmem_dealloc_pair(tmem, S::kTmemCols);
@@ -943,12 +981,18 @@ cudaError_t launch_int8_mm(const void* x_q, const float* x_scales, const void* w
   a.K = (int)K;
   a.kblocks = (int)((K + kBK - 1) / kBK);
   a.prefetch = prefetch;
+  a.wait_ns = testing_wait_ns();
+  a.delay_ns = testing_delay_ns();
   return dtype == AQ_F16 ? by_plan<__half>(p, x_q, w_q, a, st)
                          : by_plan<__nv_bfloat16>(p, x_q, w_q, a, st);
 }
 
 cudaError_t read_device_error_int8(unsigned* out) {
   return cudaMemcpyFromSymbol(out, g_int8_device_error, sizeof(unsigned));
+}
+cudaError_t testing_clear_device_error_int8() {
+  const unsigned z = 0;
+  return cudaMemcpyToSymbol(g_int8_device_error, &z, sizeof(z));
 }
 
 void testing_set_int8_plan(int bn, int pair, int splits) {

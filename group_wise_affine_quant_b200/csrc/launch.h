@@ -125,6 +125,7 @@ cudaError_t launch_int8_mm(const void* x_q, const float* x_scales, const void* w
                            const float* w_scales, void* y, int64_t M, int64_t N, int64_t K,
                            int dtype, int prefetch, cudaStream_t st);
 cudaError_t read_device_error_int8(unsigned* out);
+cudaError_t testing_clear_device_error_int8();
 void testing_set_int8_plan(int bn, int pair, int splits);
 
 // Mixture-of-experts layer for a few tokens (moe.cu).

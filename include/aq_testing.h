@@ -9,8 +9,8 @@
  * the other roles run out.  The pages have no counterpart.
  *
  * Scope: the bounded waits of the warp-MMA decode kernel behind aq_qmv /
- * aq_qmv_batched / aq_qmv_noalloc (4-bit affine weights) and of the
- * mixture-of-experts kernel; aq_qmv's kernel choice,
+ * aq_qmv_batched / aq_qmv_noalloc (4-bit affine weights), of the 8-bit integer
+ * product and of the mixture-of-experts kernel; aq_qmv's kernel choice,
  * aq_gather_qmm's grouping of index pairs, and aq_int8_mm's tile.  The
  * settings are process-wide and apply to launches made after the call; 0
  * restores the default.
@@ -27,9 +27,10 @@ extern "C" {
 /* Bound of every wait of these kernels, in ns (default 2 s). */
 AQ_API void aq_testing_set_wait_limit_ns(uint64_t ns);
 
-/* Delay, in ns, before the decode kernel's TMA warp issues its first copy, or
- * before one CTA of the mixture-of-experts kernel starts (default 0).  The
- * former ends early once another role has given up. */
+/* Delay, in ns, before the TMA warp of the decode kernel issues its first copy,
+ * that of the integer product its first copy of x, or one CTA of the
+ * mixture-of-experts kernel starts (default 0).  In the first two it ends
+ * early once another role has given up. */
 AQ_API void aq_testing_set_start_delay_ns(uint64_t ns);
 
 /* Kernel that later aq_qmv calls of this process use where it applies:

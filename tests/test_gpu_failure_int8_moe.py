@@ -10,6 +10,8 @@ import torch
 
 from group_wise_affine_quant_b200 import api
 from group_wise_affine_quant_b200._lib import AQ_OK, lib
+from tests.gpu_util import DEV
+from tests.test_gpu_int8 import codes, mm_ref, scales
 from tests.test_gpu_moe import Layer
 
 pytestmark = pytest.mark.gpu
@@ -53,5 +55,39 @@ def test_moe_scratch_serves_again(router, own_workspace):
             assert int(space.get(x.device, 1)[:65536].count_nonzero()) == 0
         got = [call() for _ in range(3)]
         assert all(torch.equal(y, want) for y in got)
+    torch.cuda.synchronize()
+    assert lib().aq_device_errors() == 0
+
+
+@pytest.mark.parametrize("tokens,pair,splits", [(16, 0, 1), (32, 0, 4), (64, 0, 8), (128, 0, 1), (128, 1, 1),
+                                                (256, 1, 1)])
+@pytest.mark.parametrize("M,N,K", [(40, 300, 272), (600, 1000, 4096)])
+def test_int8_mm_returns_and_serves_again(tokens, pair, splits, M, N, K):
+    """The products' and the stores' waits run out while the TMA warp is held back;
+    it then finds the flag.  K = 272: all copies fit the ring, so that the warp
+    ends with copies in flight; 4096: it gives up on its own wait."""
+    xq, wq, xs, ws = codes(M, K, 1), codes(N, K, 2), scales(M, 1), scales(N, 2)
+    want = mm_ref(xq, xs, wq, ws, torch.bfloat16)
+    room = torch.full((M * N + 128,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = room[64:64 + M * N].view(M, N)
+    try:
+        lib().aq_testing_set_int8_plan(tokens, pair, splits)
+        with waits_run_out():
+            api.aq_int8_mm(xq, xs, wq, ws, out=out)
+        for _ in range(2):
+            assert torch.equal(api.aq_int8_mm(xq, xs, wq, ws, out=out), want)
+    finally:
+        lib().aq_testing_set_int8_plan(0, 0, 0)
+    assert (room[:64] == 7).all() and (room[64 + M * N:] == 7).all()
+    assert lib().aq_device_errors() == 0
+
+
+def test_qqmm_int8_after_a_time_out():
+    x = torch.randn((9, 1024), device=DEV).to(torch.bfloat16)
+    wq, ws = api.aq_quantize_int8(torch.randn((512, 1024), device=DEV).to(torch.bfloat16))
+    want = api.aq_qqmm_int8(x, wq, ws)
+    with waits_run_out():
+        api.aq_qqmm_int8(x, wq, ws)
+    assert torch.equal(api.aq_qqmm_int8(x, wq, ws), want)
     torch.cuda.synchronize()
     assert lib().aq_device_errors() == 0
