@@ -522,6 +522,7 @@ def _moe_out(x, out, T, H):
 
 
 _Nine = ctypes.c_uint64 * 9
+_MAX_TOP_K = 16
 
 
 def aq_moe(x, w_router, gate, up, down, top_k, normalize=True, bits=4, group_size=64, out=None,
@@ -539,7 +540,8 @@ def aq_moe(x, w_router, gate, up, down, top_k, normalize=True, bits=4, group_siz
     if dev != _current_device():
         with torch.cuda.device(dev):
             return aq_moe(x, w_router, gate, up, down, top_k, normalize, bits, group_size, out, workspace)
-    k = max(int(top_k), 0)
+    top_k = max(min(int(top_k), 1 << 62), -1)   # what a 64-bit argument holds
+    k = min(max(top_k, 0), _MAX_TOP_K)          # more are refused below, not allocated first
     indices = torch.empty(T, k, dtype=torch.int32, device=x.device)
     weights = torch.empty(T, k, dtype=torch.float32, device=x.device)
     buf, ws, nbytes = _workspace(workspace, x, _moe_bytes(T, H, I, E, k), True)
