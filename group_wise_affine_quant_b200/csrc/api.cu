@@ -849,8 +849,8 @@ int aq_testing_gather_groups(const int32_t* lhs_indices, const int32_t* rhs_indi
 
 void aq_testing_set_wait_limit_ns(uint64_t ns) { aq::testing_set_wait_ns(ns); }
 void aq_testing_set_start_delay_ns(uint64_t ns) { aq::testing_set_delay_ns(ns); }
-void aq_testing_set_int8_plan(int tokens, int pair, int splits) {
-  aq::testing_set_int8_plan(tokens, pair, splits);
+void aq_testing_set_int8_plan(int columns, int pair, int splits) {
+  aq::testing_set_int8_plan(columns, pair, splits);
 }
 void aq_testing_set_qmv_kernel(int which) { g_qmv_kernel.store(which, std::memory_order_relaxed); }
 aq_status aq_testing_clear_device_errors(void) {

@@ -8,13 +8,14 @@
 // between the two passes up to K = 16384 (longer rows are read twice, the
 // second time from L2): 2 bytes in and 1 out per element.  The maximum is
 // taken on the 16-bit patterns without their sign (NaN > inf > finite).  What
-// bounds it is HBM: 8192 x 4096 bf16 20.0 us, 5.0 TB/s.
+// bounds it is HBM: 8192 x 4096 bf16 19.2 us, 5.2 TB/s.
 //
 // Product: y[m, n] = T(((float)sum_k x_q w_q * s_x[m]) * s_w[n]).  The sum is
 // exact in 32-bit integers (K is limited so that it cannot overflow),
 // whatever the split; the conversion to fp32 rounds by at most 2^-24.  Tensor
-// cores bound large products (8192 x 8192 x 2048 89 us, 3.1 POP/s; 109 us under
-// the power cap), a tile's start and end small ones (1 x 2048 x 2048 3.9 us).
+// cores bound large products (8192 x 8192 x 2048 93 us, 3.0 POP/s; 107 us in a
+// loop under the power cap), a tile's start and end small ones (1 x 2048 x 2048
+// 4.1 us, from HBM 4.5).
 #include <atomic>
 #include <cooperative_groups.h>
 
@@ -224,7 +225,7 @@ cudaError_t quantize_rows(const void* x, void* xq, float* scales, int64_t rows, 
 //     holds a token's run of channels, which leaves through shared memory in
 //     TMA stores (rows of y of odd length: by the warps).
 constexpr int kBK = 128;                 // bytes (elements) of K per stage
-constexpr int kBM = 128;                 // channels per CTA
+constexpr int kBM = 128;                 // rows of the A operand per CTA: channels, kPair: tokens
 
 template <int BN, bool PAIR>
 struct MmShape {
@@ -903,7 +904,7 @@ cudaError_t by_plan(const Int8Plan& p, const void* x_q, const void* w_q, const M
   }
 }
 
-// Plan forced by a test: tokens per tile (0: automatic), pair, K-slices.
+// Plan forced by a test: Int8Plan's bn (0: automatic), pair, K-slices.
 std::atomic<int> g_force_bn{0}, g_force_pair{0}, g_force_splits{0};
 
 }  // namespace
@@ -916,7 +917,7 @@ std::atomic<int> g_force_bn{0}, g_force_pair{0}, g_force_splits{0};
 // Clusters do not fill the GPU: `slots` is how many run at once.
 Int8Plan plan_int8_mm(int64_t M, int64_t N, int64_t K) {
   struct Tile {
-    int bn;
+    int bn;                              // as in Int8Plan
     bool pair;
     int block, full, start, column;      // clocks: per block, more at full load, start, per column
   };

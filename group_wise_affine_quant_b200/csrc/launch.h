@@ -112,8 +112,8 @@ cudaError_t read_device_error_conv(unsigned* out);
 
 // W8A8 (int8.cu): row quantizer and integer product.
 struct Int8Plan {
-  int bn;          // tokens per tile (MMA N)
-  bool pair;       // two CTAs share a tile of 256 channels
+  int bn;          // MMA N: tokens per tile (128 channels), in a pair channels
+  bool pair;       // two CTAs share a tile of 256 tokens
   int splits;      // K-slices, one cluster per tile
   int kb_split;    // 128-element blocks of K per slice
   int64_t groups;  // CTA pairs, clusters or CTAs launched

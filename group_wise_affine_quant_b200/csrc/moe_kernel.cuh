@@ -19,20 +19,24 @@
 // tiles; a team of 2 to 16 of its warps shares the K of one, so each warp
 // keeps its part of x in registers over all row tiles of a token tile and
 // streams its part of the weight rows by cp.async through a ring of its own.
-// The warps' sums meet in shared memory after four row tiles per team (with two
-// 16 tokens, 8 of 64 experts of 2048 x 1408 in 4 bits take 116 us, with four 109).
+// The warps' sums meet in shared memory after four row tiles per team (16 tokens,
+// 8 of 64 experts of 2048 x 1408 in 4 bits take 96 us, after two row tiles 105).
 //
-// Measured: that layer 97 us, 2.8 TB/s of its 275 MB (token tiles of 4 took it
-// there from 109): the issue slots and latencies of unpacking, about 55
-// instructions for 16 x 32 codes where the HBM rate leaves 45.  One token, 8 of
-// 64 experts of 2048 x 768: 22 us, most of it dependent steps.
+// Measured: that layer 96 us, 2.9 TB/s of its 275 MB (with token tiles of 8 only,
+// 107): the issue slots and latencies of unpacking, about 53 instructions for
+// 16 x 32 codes where the HBM rate leaves 45.  One token, 8 of 64 experts of
+// 2048 x 768: 22 us (from HBM 24.5), most of it dependent steps.
 //
 // The codes become the A operand of mma.m16n8k16 as exact small numbers and x
 // the B operand; per group the products P and the sums X of x leave in fp32:
 //   sum += s P + (b - offset s) X,      P = sum (offset + q) x.
-// So w_hat is never rounded to T.  h is kept as two bf16 numbers (hi + lo, 16
-// bits of significand), in the B operand's order, so that down's operand
-// rounds far below T.  Each pair (token, slot) has its row of fp32 results;
+// So w_hat is never rounded to T.  In bf16 operands the offset is 128, which takes
+// 4 (4 bits) to 6 (2 bits) of the 24 bits of these sums: the rest rounds far
+// below T, and codes of up to 4 bits beside 16 instead of 128, three bits better,
+// cost a shift a word (97.2 us instead of 95.9; the results are as far from the
+// 64-bit values, 1.66e-3 of them in bf16, either way).  h is kept as two bf16
+// numbers (hi + lo, 16 bits of significand), in the B operand's order, so that
+// down's operand rounds far below T.  Each pair (token, slot) has its row of fp32 results;
 // the last step adds them in slot order, so no atomics touch a sum and equal
 // inputs give equal outputs.
 #pragma once
@@ -604,7 +608,6 @@ struct Phase {
   using O = typename std::conditional<PH == 1, T, __nv_bfloat16>::type;
   static constexpr int kGu = F::kGs >= 32 ? F::kGs / 32 : 1;     // chunks per group
   static constexpr int kParts = F::template kHeld<1> / kGu;      // groups held, at most
-  static constexpr int kArrays = F::kFp4 ? 1 : 2;
   // The sums of x over groups of 32 would take 16 registers more than there are:
   // they are made again with each row tile, by an MMA beside the codes'.
   static constexpr bool kSumsInPlace = !F::kFp4 && kParts > 4;

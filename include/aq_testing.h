@@ -42,10 +42,11 @@ AQ_API void aq_testing_set_start_delay_ns(uint64_t ns);
 AQ_API void aq_testing_set_qmv_kernel(int which);
 
 /* Tile that later aq_int8_mm / aq_qqmm_int8 calls of this process use:
- * `tokens` per tile (16, 32, 64 or 128; 128 or 256 with `pair`, two CTAs to a
- * tile) and at most `splits` K-slices (1..8, without `pair`).  0 tokens: the
- * automatic choice (default). */
-AQ_API void aq_testing_set_int8_plan(int tokens, int pair, int splits);
+ * `columns` of its MMAs (16, 32, 64 or 128 tokens against 128 channels; with
+ * `pair`, two CTAs to a tile, 128 or 256 channels against 256 tokens) and at
+ * most `splits` K-slices (1..8, without `pair`).  0 columns: the automatic
+ * choice (default). */
+AQ_API void aq_testing_set_int8_plan(int columns, int pair, int splits);
 
 /* The expert grouping aq_gather_qmm would use for these index pairs (host
  * logic only, no launch): returns the number of grouped problems (0 when the
